@@ -305,21 +305,23 @@ def _grad_norm(st):
     return torch.stack([n, torch.clamp(MAX_NORM / n, max=1.0)])
 
 
-def _dither(place, step, turn):
-    """The place in [0, 2^32) where element `place` rounds up at this step: a Weyl sequence."""
-    return (place.long() * 0x85EBCA6B + (step * 0x9E3779B9 + turn)) & 0xFFFFFFFF
+def _dither(place, step):
+    """16 + 16 bits for every element and step, in [0, 2^16): thresholds of m and of v."""
+    x = (place.long() * 0x85EBCA6B + step * 0x9E3779B9) & 0xFFFFFFFF
+    x = ((x ^ (x >> 15)) * 0x2C1B3C6D) & 0xFFFFFFFF
+    x = ((x ^ (x >> 12)) * 0x297A2D39) & 0xFFFFFFFF
+    x = x ^ (x >> 15)
+    return (x >> 16).to(torch.int32), (x & 0xFFFF).to(torch.int32)
 
 
-def _mx_dither(x, place, step, turn, never_zero):
+def _mx_dither(x, r, never_zero):
     """Codes and scales of x, rounded up where the element's threshold says so."""
     b = x.view(-1, 32)
     scale, inverse = _mx_scale(b)
     q = (b.abs() * inverse.unsqueeze(-1)).view(-1)
-    r = _dither(place, step, turn)
-    bits = (q.view(torch.int32) + (r >> 12).to(torch.int32)) & ~0xFFFFF      # 3 bits of mantissa
-    normal = bits.view(torch.float32)
-    small = torch.floor(q * 512.0 + (r >> 8).float() * 2.0 ** -24) * 2.0 ** -9  # multiples of 2^-9
-    q = torch.where(q < 2.0 ** -6, small, normal).clamp_(max=448.0)
+    bits = (q.view(torch.int32) + (r << 4) + 8) & ~0xFFFFF                   # 3 bits of mantissa
+    small = torch.floor(q * 512.0 + (r.float() + 0.5) * 2.0 ** -16) * 2.0 ** -9  # multiples of 2^-9
+    q = torch.where(q < 2.0 ** -6, small, bits.view(torch.float32)).clamp_(max=448.0)
     if never_zero:
         q = torch.where(x > 0, q.clamp(min=2.0 ** -9), q)
     return torch.copysign(q, x).to(torch.float8_e4m3fn), scale
@@ -341,10 +343,10 @@ def _adam_group(gr, step, clip, decay, mx):
     if "master" in gr:
         gr["param"].copy_(w)
     if mx:
-        place = gr["place"]
-        codes, scales = _mx_dither(m, place, step, 0, False)
+        rm, rv = _dither(gr["place"], step)
+        codes, scales = _mx_dither(m, rm, False)
         gr["m"].copy_(codes), gr["m_scale"].copy_(scales)
-        codes, scales = _mx_dither(v, place, step, 1 << 31, True)
+        codes, scales = _mx_dither(v, rv, True)
         gr["v"].copy_(codes), gr["v_scale"].copy_(scales)
 
 
