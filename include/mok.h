@@ -239,6 +239,148 @@ size_t mok_layer_host_extra_size(const mok_dims *dims);
 int mok_layer_forward_host(const mok_dims *dims, const mok_weights *w, const void *x_host,
                            void *y_host, void *ws, size_t ws_bytes, mok_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Around the layer: the norm in front of it, the router's auxiliary losses, gradient clipping and
+ * the optimiser.  The pages describe only the layer; these entry points carry a pre-norm residual
+ * block built on it through a training step (and its norm through a serving step).  Same
+ * conventions as above: caller-owned device memory, work enqueued on `stream`, nothing allocated,
+ * bit-identical reruns.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Element type of a tensor that may come in 16 or 32 bits. */
+typedef enum { MOK_T_BF16 = 0, MOK_T_F32 = 1 } mok_elem;
+/* Layout of MXFP8 scale bytes: [rows, K/32] row-major, or the 512-byte atoms
+ * [ceil(rows/128)][K/128] that the layer's block-scaled GEMMs read (mok_prepare_weights). */
+typedef enum { MOK_SCALES_ROWS = 0, MOK_SCALES_ATOMS = 1 } mok_scale_layout;
+
+/* RMS norm with the residual's addition: h = x + residual (x when residual is NULL),
+ * v = h / sqrt(mean(h^2) + eps) * weight per row of d elements, everything in fp32.
+ *   x[T,d] bf16, residual[T,d] of res_type (or NULL), weight[d] of weight_type
+ *   -> y[T,d] = v in bf16 (NULL to skip), residual_out[T,d] = h in res_type (required with a
+ *      residual, NULL without), and with codes != NULL the MXFP8 form of v: codes[T,d] E4M3 and
+ *      scales in scale_layout, by the rule of mok_mx_quantize_rows applied to v itself (not to
+ *      its bf16 rounding).  The atoms' padding rows (T to the next multiple of 128) are zero.
+ * At least one of y and codes.  residual_out may be residual and y may be x (in place).
+ * T >= 0, 0 < d <= 32768, d % 8 == 0 (d % 128 == 0 with codes), eps > 0; 16-byte aligned
+ * pointers.  One launch. */
+int mok_rms_norm(int64_t T, int d, float eps, const void *x, const void *residual, int res_type,
+                 const void *weight, int weight_type, void *y, void *residual_out, void *codes,
+                 void *scales, int scale_layout, mok_stream_t stream);
+
+/* Bytes of workspace of mok_rms_norm_backward (0 for invalid sizes). */
+size_t mok_rms_norm_workspace_size(int64_t T, int d);
+
+/* Gradients of mok_rms_norm.  With s[T,d] (res_type) the rows that were normalised (residual_out
+ * of the forward, or x in bf16 when there was no residual), rho = 1 / sqrt(mean(s^2) + eps)
+ * (recomputed), xhat = s rho and g = dy weight:
+ *   ds = rho (g - xhat mean(g xhat)) + dres,   dweight = sum over rows of dy xhat.
+ *   dy[T,d] bf16, dres[T,d] of res_type (the gradient that arrives through residual_out) or NULL
+ *   -> ds in bf16 in dx[T,d] (NULL to skip) and in res_type in dresidual[T,d] (NULL to skip; at
+ *      least one of the two), dweight[d] fp32 (rows summed in a fixed order).
+ * ds is the gradient of x and of the residual alike.  dx may be dy, dresidual may be dres or s.
+ * Sizes and alignment as in mok_rms_norm.  Two launches. */
+int mok_rms_norm_backward(int64_t T, int d, float eps, const void *dy, const void *s, int res_type,
+                          const void *weight, int weight_type, const void *dres, void *dx,
+                          void *dresidual, float *dweight, void *ws, size_t ws_bytes,
+                          mok_stream_t stream);
+
+/* Bytes of workspace of mok_balance_loss for n_seqs sequences (0 for invalid sizes). */
+size_t mok_balance_loss_workspace_size(const mok_dims *dims, int64_t n_seqs);
+
+/* Balance loss and z loss of the router, per-expert counts and the gradient of the logits.
+ * Tokens seq_offsets[s] <= t < seq_offsets[s+1] form sequence s; a token whose token_mask byte is
+ * 0, or that is in no sequence, is left out of everything.  With p_t = softmax(logits_t),
+ * n the number of valid tokens, n_s those of sequence s and c[s,e] how many of them chose e:
+ *   balance = alpha sum_s (n_s / n) sum_e f[s,e] P[s,e],  f[s,e] = E c[s,e] / (k n_s),
+ *             P[s,e] = the mean of p_t[e] over the sequence's valid tokens;
+ *   z       = z_coef / n sum_t (log sum_e exp(logits_t[e]))^2;
+ *   dlogits = grad d(balance + z)/d logits, the selection (and so c) held constant.
+ *   logits[T,E] fp32, topk_idx[T,k] int32 (both from mok_route), seq_offsets[n_seqs+1] int32
+ *   ascending on the device (NULL: one sequence of all tokens, n_seqs == 1), token_mask[T] bytes
+ *   or NULL, grad a device scalar or NULL (1)
+ *   -> counts[n_seqs,E] int32, loss[2] fp32 = {balance, z}, dlogits[T,E] fp32 (NULL to skip; rows
+ *      of left-out tokens are zero, whatever their logits hold).
+ * Experts masked with -inf logits get probability and gradient 0; a token all of whose logits are
+ * -inf gives no loss and no gradient.  An index outside [0,E) sets MOK_ERR_DEVICE_CHECK in the
+ * status word of ws and its route is not counted.  dims->T, E, k are used; n_seqs >= 1,
+ * n_seqs * E < 2^31.  The gradient goes into mok_moe_backward_aux. */
+int mok_balance_loss(const mok_dims *dims, const float *logits, const int32_t *topk_idx,
+                     const int32_t *seq_offsets, int64_t n_seqs, const uint8_t *token_mask,
+                     float alpha, float z_coef, const float *grad, int32_t *counts, float *loss,
+                     float *dlogits, void *ws, size_t ws_bytes, mok_stream_t stream);
+
+/* Bytes of workspace of mok_grad_norm for tensors of these element counts (0 when invalid). */
+size_t mok_grad_norm_workspace_size(int n_tensors, const int64_t *numel);
+
+/* Norm of all gradients together: out[2] fp32 on the device = {norm, factor} with norm the root
+ * of the sum of squares over every tensor (fp32 partial sums in a fixed order, joined in 64 bits)
+ * and factor = min(1, max_norm / norm) (1 when max_norm <= 0, NaN when the norm is not finite).
+ * grads, numel and types (mok_elem) are HOST arrays of n_tensors entries; they may be reused as
+ * soon as the call returns.  Tensors are 16-byte aligned; empty ones are fine. */
+int mok_grad_norm(int n_tensors, const void *const *grads, const int64_t *numel,
+                  const int32_t *types, float max_norm, float *out, void *ws, size_t ws_bytes,
+                  mok_stream_t stream);
+
+/* Format of the AdamW states.  MOK_STATE_MXFP8: E4M3 codes [numel] and one UE8M0 byte per 32
+ * consecutive elements [ceil(numel/32)], scale rule of mok_mx_quantize_rows, dithered rounding:
+ * element i goes to the upper of its two neighbouring codes when its place between them plus
+ * (r + 1/2) / 2^16 reaches 1.  With x = 0x85EBCA6B i + 0x9E3779B9 step, x ^= x >> 15,
+ * x *= 0x2C1B3C6D, x ^= x >> 12, x *= 0x297A2D39, x ^= x >> 15 (all mod 2^32), r is x's high half
+ * for exp_avg and its low half for exp_avg_sq.  The mean over steps is the value, so averages
+ * that move by less than half a code per step still move.  exp_avg_sq > 0 never takes code 0. */
+typedef enum { MOK_STATE_F32 = 0, MOK_STATE_MXFP8 = 1 } mok_state_format;
+
+/* One tensor of mok_adamw_step (device pointers, 16-byte aligned; the scales need not be). */
+typedef struct {
+  void *param;               /* [numel] of param_type, updated */
+  const void *grad;          /* [numel] of grad_type */
+  float *master;             /* [numel] fp32 copy of a bf16 param, updated; NULL for an fp32 one */
+  void *exp_avg;             /* [numel] fp32 or E4M3 codes, updated */
+  void *exp_avg_sq;          /* [numel] likewise */
+  uint8_t *exp_avg_scale;    /* [ceil(numel/32)], NULL for MOK_STATE_F32 */
+  uint8_t *exp_avg_sq_scale;
+  int64_t numel;
+  double weight_decay;
+  int32_t param_type;        /* mok_elem */
+  int32_t grad_type;
+} mok_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;              /* 1 for the first step */
+  int32_t state_format;      /* mok_state_format */
+} mok_adamw_args;
+
+/* One AdamW step over all tensors: with g = factor grad (factor = clip[1], or 1 when clip is
+ * NULL), m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2,
+ *   w = w - lr (m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps) + weight_decay w),
+ * all in fp32 on the master (or the fp32 param); a bf16 param is the rounded master.  `tensors`
+ * is a HOST array, free for reuse when the call returns; clip is the device output of
+ * mok_grad_norm: when its factor is NaN (a norm that is not finite) the step leaves everything
+ * unchanged.  0 <= beta < 1, eps > 0, step >= 1. */
+int mok_adamw_step(const mok_adamw_args *args, const mok_adamw_tensor *tensors, int n_tensors,
+                   const float *clip, mok_stream_t stream);
+
+/* mok_moe_forward for MOK_MXFP8 with x already quantised: x_codes[T,d] and x_scales (atoms,
+ * T rows x d) as mok_rms_norm or the layer's own quantiser write them; skips the layer's pass
+ * over x.  Same outputs as mok_moe_forward on the same codes.  MOK_ERR_UNSUPPORTED for another
+ * dtype. */
+int mok_moe_forward_mx(const mok_dims *dims, const mok_weights *w, const void *x_codes,
+                       const void *x_scales, const int32_t *topk_idx, const int32_t *offsets,
+                       const int32_t *sorted_tok, const float *sorted_w, const int32_t *inv_pos,
+                       void *y, void *saved, void *ws, size_t ws_bytes, mok_stream_t stream);
+
+/* mok_moe_backward with a further gradient of the logits (dlogits_aux[T,E] fp32, from
+ * mok_balance_loss; NULL: exactly mok_moe_backward), added in fp32 before dlogits is used: dX and
+ * dW_router include it and the output dlogits is the sum. */
+int mok_moe_backward_aux(const mok_dims *dims, const mok_weights *w, const void *x, const void *dY,
+                         const void *saved, const int32_t *topk_idx, const float *topk_w,
+                         const int32_t *offsets, const int32_t *sorted_tok, const float *sorted_w,
+                         const int32_t *inv_pos, const float *dlogits_aux, void *dX, void *dW_gate,
+                         void *dW_up, void *dW_down, void *dWs_gate, void *dWs_up, void *dWs_down,
+                         float *dlogits, void *dW_router, void *ws, size_t ws_bytes,
+                         mok_stream_t stream);
+
 /* Schedule of the bf16 expert GEMMs of mok_moe_forward (process-wide; default
  * MOK_SCHEDULE_TWO_LAUNCHES):
  *  - MOK_SCHEDULE_TWO_LAUNCHES: gate/up + SwiGLU, then down + router weight, each one persistent

@@ -7,7 +7,8 @@ kernels.  There is no fallback: without the compiled library every call raises.
 
 Entry points mirror the C ABI: :func:`route`, :func:`dispatch_index`, :func:`moe_forward`,
 :func:`moe_backward`, :func:`layer_forward_host`, plus :class:`MoELayer`, a small convenience
-holder of weights and workspaces.
+holder of weights and workspaces.  Around the layer: :func:`rms_norm`, :func:`balance_loss`,
+:func:`grad_norm` and :class:`AdamW`, and :class:`MoEBlock`, which runs them together.
 """
 
 import ctypes
@@ -21,6 +22,9 @@ __all__ = [
     "read_status", "clear_status", "last_launch_count", "MoELayer", "EXPORTED_SYMBOLS",
     "MOK_BF16", "MOK_MXFP8", "MOK_NVFP4", "prepare_weights", "prepare_weights_bwd",
     "mx_quantize_rows", "nvfp4_set_activation_amax",
+    "rms_norm", "rms_norm_backward", "rms_norm_workspace_size", "balance_loss",
+    "balance_loss_workspace_size", "TensorList", "grad_norm", "grad_norm_workspace_size", "AdamW",
+    "MoEBlock",
 ]
 
 MOK_BF16, MOK_MXFP8, MOK_NVFP4 = 0, 1, 2
@@ -34,6 +38,9 @@ EXPORTED_SYMBOLS = [
     "mok_timing_enable", "mok_timing_collect", "mok_dispatch_index_noalloc",
     "mok_mx_quantize_rows", "mok_selftest_bounded_wait", "mok_prepared_bwd_size",
     "mok_prepare_weights_bwd", "mok_set_forward_schedule", "mok_nvfp4_set_activation_amax",
+    "mok_rms_norm", "mok_rms_norm_workspace_size", "mok_rms_norm_backward",
+    "mok_balance_loss_workspace_size", "mok_balance_loss", "mok_grad_norm_workspace_size",
+    "mok_grad_norm", "mok_adamw_step", "mok_moe_forward_mx", "mok_moe_backward_aux",
 ]
 
 
@@ -53,9 +60,22 @@ class Weights(ctypes.Structure):
         "prepared", "prepared_bwd")]
 
 
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "param", "grad", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")] + [
+        ("numel", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+        ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32)]
+
+
+class AdamWArgs(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("state_format", ctypes.c_int32)]
+
+
 _LIB = None
 _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
+_I64, _INT, _F = ctypes.c_int64, ctypes.c_int, ctypes.c_float
 _DP = ctypes.POINTER(Dims)
 _WP = ctypes.POINTER(Weights)
 
@@ -95,6 +115,16 @@ def lib():
             "mok_dispatch_index_noalloc": (ctypes.c_int, [_DP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
             "mok_set_forward_schedule": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_int)]),
             "mok_nvfp4_set_activation_amax": (ctypes.c_int, [_DP, _VP, ctypes.c_float, ctypes.c_float, _VP]),
+            "mok_rms_norm": (ctypes.c_int, [_I64, _INT, _F, _VP, _VP, _INT, _VP, _INT, _VP, _VP, _VP, _VP, _INT, _VP]),
+            "mok_rms_norm_workspace_size": (_SZ, [_I64, _INT]),
+            "mok_rms_norm_backward": (ctypes.c_int, [_I64, _INT, _F, _VP, _VP, _INT, _VP, _INT] + [_VP] * 5 + [_SZ, _VP]),
+            "mok_balance_loss_workspace_size": (_SZ, [_DP, _I64]),
+            "mok_balance_loss": (ctypes.c_int, [_DP, _VP, _VP, _VP, _I64, _VP, _F, _F] + [_VP] * 5 + [_SZ, _VP]),
+            "mok_grad_norm_workspace_size": (_SZ, [_INT, _VP]),
+            "mok_grad_norm": (ctypes.c_int, [_INT, _VP, _VP, _VP, _F, _VP, _VP, _SZ, _VP]),
+            "mok_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamWArgs), ctypes.POINTER(AdamWTensor), _INT, _VP, _VP]),
+            "mok_moe_forward_mx": (ctypes.c_int, [_DP, _WP] + [_VP] * 10 + [_SZ, _VP]),
+            "mok_moe_backward_aux": (ctypes.c_int, [_DP, _WP] + [_VP] * 20 + [_SZ, _VP]),
             "mok_timing_collect": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_int),
                                                   ctypes.POINTER(ctypes.c_double), ctypes.c_int,
                                                   ctypes.POINTER(ctypes.c_int)]),
@@ -293,6 +323,125 @@ def mx_quantize_rows(src):
     return q, sc
 
 
+_ELEM = {torch.bfloat16: 0, torch.float32: 1}   # mok_elem
+
+
+def _elem(t, name):
+    if t.dtype not in _ELEM:
+        raise ValueError(f"{name}: dtype {t.dtype} is neither bfloat16 nor float32")
+    return _ELEM[t.dtype]
+
+
+def _scale_bytes(rows, K, layout):
+    return (rows + 127) // 128 * 128 * (K // 32) if layout == "atoms" else rows * (K // 32)
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, mx=None, want_y=True):
+    """RMS norm of the rows of x [T,d] bf16, with the residual's addition: h = x + residual,
+    v = h / sqrt(mean(h^2) + eps) * weight, in fp32.  residual [T,d] and weight [d] are bf16 or
+    fp32.  Returns a dict: "y" (v in bf16; not with want_y=False), "residual" (h in residual's
+    type, when there is one) and, with mx="rows" or "atoms", the MXFP8 form of v: "codes" uint8
+    [T,d] and "scales" uint8 ([T,d/32], or the flat scale atoms that
+    ``moe_forward(..., x_mx=(codes, scales))`` takes)."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    T, d = x.shape
+    dev = x.device
+    _want(x, "x", (T, d), torch.bfloat16, dev)
+    _want(weight, "weight", (d,), weight.dtype, dev)
+    wt = _elem(weight, "weight")
+    if mx not in (None, "rows", "atoms"):
+        raise ValueError("mx must be None, 'rows' or 'atoms'")
+    out = {}
+    if want_y:
+        out["y"] = torch.empty_like(x)
+    rt = 0
+    if residual is not None:
+        rt = _elem(residual, "residual")
+        _want(residual, "residual", (T, d), residual.dtype, dev)
+        out["residual"] = torch.empty_like(residual)
+    if mx is not None:
+        out["codes"] = torch.empty((T, d), dtype=torch.uint8, device=dev)
+        n = _scale_bytes(T, d, mx)
+        out["scales"] = torch.empty((T, d // 32) if mx == "rows" else (n,), dtype=torch.uint8, device=dev)
+    _check(lib().mok_rms_norm(T, d, eps, _ptr(x), _ptr(residual), rt, _ptr(weight), wt,
+                              _ptr(out.get("y")), _ptr(out.get("residual")), _ptr(out.get("codes")),
+                              _ptr(out.get("scales")), 1 if mx == "atoms" else 0, _stream()))
+    return out
+
+
+def rms_norm_workspace_size(T, d):
+    n = lib().mok_rms_norm_workspace_size(T, d)
+    if n == 0:
+        raise MokError("unsupported norm dimensions")
+    return n
+
+
+def rms_norm_backward(dy, s, weight, eps=1e-6, dres=None, ws=None):
+    """Gradients of :func:`rms_norm`: dy [T,d] bf16 of "y"; s the rows that were normalised (its
+    "residual", or x when there was none); dres the gradient that arrives through "residual" (of
+    s's type) or None.  Returns a dict: "dx" [T,d] bf16 (the gradient of x, and of a bf16
+    residual), "dresidual" [T,d] fp32 when s is fp32, "dweight" [d] fp32.  ``ws``: at least
+    rms_norm_workspace_size(T, d) bytes (allocated per call when None)."""
+    if s.dim() != 2:
+        raise ValueError("s must be 2-D")
+    T, d = s.shape
+    dev = s.device
+    st, wt = _elem(s, "s"), _elem(weight, "weight")
+    _want(s, "s", (T, d), s.dtype, dev)
+    _want(dy, "dy", (T, d), torch.bfloat16, dev)
+    _want(weight, "weight", (d,), weight.dtype, dev)
+    if dres is not None:
+        _want(dres, "dres", (T, d), s.dtype, dev)
+    if ws is None:
+        ws = torch.empty(rms_norm_workspace_size(T, d), dtype=torch.uint8, device=dev)
+    out = {"dx": torch.empty_like(dy), "dweight": torch.empty((d,), dtype=torch.float32, device=dev)}
+    if st:
+        out["dresidual"] = torch.empty_like(s)
+    _check(lib().mok_rms_norm_backward(T, d, eps, _ptr(dy), _ptr(s), st, _ptr(weight), wt, _ptr(dres),
+                                       _ptr(out["dx"]), _ptr(out.get("dresidual")), _ptr(out["dweight"]),
+                                       _ptr(ws), ws.numel(), _stream()))
+    return out
+
+
+def balance_loss_workspace_size(D, n_seqs=1):
+    n = lib().mok_balance_loss_workspace_size(ctypes.byref(D), n_seqs)
+    if n == 0:
+        raise MokError("unsupported layer dimensions")
+    return n
+
+
+def balance_loss(D, logits, topk_idx, ws, alpha, z_coef=0.0, seq_offsets=None, token_mask=None,
+                 grad=None, want_dlogits=True):
+    """Balance loss and z loss of the router (formulas in mok.h, mok_balance_loss) for logits
+    [T,E] fp32 and topk_idx [T,k] int32 of :func:`route`.  ``seq_offsets`` int32 [S+1]: packed
+    sequences, each balanced by itself (None: one); ``token_mask`` bool [T]: tokens that count;
+    ``grad`` fp32 [1]: the upstream gradient (None: 1); ``ws``: a zeroed workspace of at least
+    balance_loss_workspace_size(D, S) bytes, whose status word reports an index outside [0,E).
+    Returns a dict: "loss" fp32 [2] (balance, z), "counts" int32 [S,E] and "dlogits" fp32 [T,E],
+    which goes into ``moe_backward(..., dlogits_aux=...)``."""
+    dev = logits.device
+    _want(logits, "logits", (D.T, D.E), torch.float32, dev)
+    _want(topk_idx, "topk_idx", (D.T, D.k), torch.int32, dev)
+    S = 1
+    if seq_offsets is not None:
+        S = seq_offsets.numel() - 1
+        _want(seq_offsets, "seq_offsets", (max(S, 1) + 1,), torch.int32, dev)
+    if token_mask is not None:
+        _want(token_mask, "token_mask", (D.T,), torch.bool, dev)
+    if grad is not None:
+        _want(grad, "grad", (1,), torch.float32, dev)
+    out = {"loss": torch.empty((2,), dtype=torch.float32, device=dev),
+           "counts": torch.empty((S, D.E), dtype=torch.int32, device=dev)}
+    if want_dlogits:
+        out["dlogits"] = torch.empty_like(logits)
+    _check(lib().mok_balance_loss(ctypes.byref(D), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), S,
+                                  _ptr(token_mask), alpha, z_coef, _ptr(grad), _ptr(out["counts"]),
+                                  _ptr(out["loss"]), _ptr(out.get("dlogits")), _ptr(ws), ws.numel(),
+                                  _stream()))
+    return out
+
+
 def prepared_size(D):
     return lib().mok_prepared_size(ctypes.byref(D))
 
@@ -335,13 +484,25 @@ def prepare_weights_bwd(D, W):
     return buf
 
 
-def moe_forward(D, W, x, routing, ws, saved=None, y=None):
-    """y[T,d] bf16 of the expert part for a routing from :func:`dispatch_index`."""
+def moe_forward(D, W, x, routing, ws, saved=None, y=None, x_mx=None):
+    """y[T,d] bf16 of the expert part for a routing from :func:`dispatch_index`.  ``x_mx``
+    (MOK_MXFP8): x already quantised, (codes uint8 [T,d], scale atoms) as :func:`rms_norm` gives
+    them with ``mx="atoms"``; the experts then read these instead of quantising x."""
     dev = x.device
     _want(x, "x", (D.T, D.d), torch.bfloat16, dev)
     ws_struct = _weights_struct(D, W)
     if y is None:
         y = torch.empty((D.T, D.d), dtype=torch.bfloat16, device=dev)
+    if x_mx is not None:
+        codes, atoms = x_mx
+        _want(codes, "x_mx codes", (D.T, D.d), torch.uint8, dev)
+        _want(atoms, "x_mx scales", (_scale_bytes(D.T, D.d, "atoms"),), torch.uint8, dev)
+        _check(lib().mok_moe_forward_mx(
+            ctypes.byref(D), ctypes.byref(ws_struct), _ptr(codes), _ptr(atoms),
+            _ptr(routing["topk_idx"]), _ptr(routing["offsets"]), _ptr(routing["sorted_tok"]),
+            _ptr(routing["sorted_w"]), _ptr(routing["inv_pos"]), _ptr(y), _ptr(saved), _ptr(ws),
+            ws.numel(), _stream()))
+        return y
     _check(lib().mok_moe_forward(
         ctypes.byref(D), ctypes.byref(ws_struct), _ptr(x), _ptr(routing["topk_idx"]),
         _ptr(routing["offsets"]), _ptr(routing["sorted_tok"]), _ptr(routing["sorted_w"]),
@@ -349,11 +510,15 @@ def moe_forward(D, W, x, routing, ws, saved=None, y=None):
     return y
 
 
-def moe_backward(D, W, x, dY, saved, routing, ws, want_dW_router=True):
-    """Gradients of the layer for upstream dY (selection held constant).  Returns a dict."""
+def moe_backward(D, W, x, dY, saved, routing, ws, want_dW_router=True, dlogits_aux=None):
+    """Gradients of the layer for upstream dY (selection held constant).  Returns a dict.
+    ``dlogits_aux`` [T,E] fp32: a further gradient of the logits (from :func:`balance_loss`),
+    included in dX, dW_router and dlogits."""
     dev = x.device
     bf = torch.bfloat16
     _want(dY, "dY", (D.T, D.d), bf, dev)
+    if dlogits_aux is not None:
+        _want(dlogits_aux, "dlogits_aux", (D.T, D.E), torch.float32, dev)
     ws_struct = _weights_struct(D, W)
     g = {
         "dX": torch.empty((D.T, D.d), dtype=bf, device=dev),
@@ -367,10 +532,10 @@ def moe_backward(D, W, x, dY, saved, routing, ws, want_dW_router=True):
         "dW_router": torch.empty((D.d, D.E), dtype=bf, device=dev) if want_dW_router else None,
     }
     r = routing
-    _check(lib().mok_moe_backward(
+    _check(lib().mok_moe_backward_aux(
         ctypes.byref(D), ctypes.byref(ws_struct), _ptr(x), _ptr(dY), _ptr(saved), _ptr(r["topk_idx"]),
         _ptr(r["topk_w"]), _ptr(r["offsets"]), _ptr(r["sorted_tok"]), _ptr(r["sorted_w"]),
-        _ptr(r["inv_pos"]), _ptr(g["dX"]), _ptr(g["dW_gate"]), _ptr(g["dW_up"]), _ptr(g["dW_down"]),
+        _ptr(r["inv_pos"]), _ptr(dlogits_aux), _ptr(g["dX"]), _ptr(g["dW_gate"]), _ptr(g["dW_up"]), _ptr(g["dW_down"]),
         _ptr(g["dWs_gate"]), _ptr(g["dWs_up"]), _ptr(g["dWs_down"]), _ptr(g["dlogits"]),
         _ptr(g["dW_router"]), _ptr(ws), ws.numel(), _stream()))
     return g
@@ -401,22 +566,29 @@ class MoELayer:
         self.saved = None
         self._ws_bwd = None
 
-    def forward(self, x, training=False):
-        idx, w, _ = route(self.D, x, self.W["W_router"], self.W.get("bias"), self.ws)
+    def forward(self, x, training=False, x_mx=None, want_logits=False):
+        idx, w, self.logits = route(self.D, x, self.W["W_router"], self.W.get("bias"), self.ws,
+                                    want_logits)
         n = last_launch_count()
         routing = dispatch_index(self.D, idx, w, self.ws)
         n += last_launch_count()
         if training and self.saved is None:
             self.saved = torch.empty(saved_size(self.D), dtype=torch.uint8, device=x.device)
-        y = moe_forward(self.D, self.W, x, routing, self.ws, saved=self.saved if training else None)
+        y = moe_forward(self.D, self.W, x, routing, self.ws, saved=self.saved if training else None,
+                        x_mx=x_mx)
         self.last_launches = n + last_launch_count()  # kernels this call enqueued
         self.routing = routing
         return y
 
-    def backward(self, x, dY):
+    def backward(self, x, dY, dlogits_aux=None):
         if self._ws_bwd is None:
             self._ws_bwd = torch.zeros(workspace_size(self.D, backward=True), dtype=torch.uint8,
                                        device=x.device)
-        g = moe_backward(self.D, self.W, x, dY, self.saved, self.routing, self._ws_bwd)
+        g = moe_backward(self.D, self.W, x, dY, self.saved, self.routing, self._ws_bwd,
+                         dlogits_aux=dlogits_aux)
         self.last_launches = last_launch_count()
         return g
+
+
+from .block import MoEBlock  # noqa: E402
+from .optim import AdamW, TensorList, grad_norm, grad_norm_workspace_size  # noqa: E402

@@ -13,6 +13,7 @@
 namespace mok {
 
 static thread_local int g_last_launches = 0;
+void set_last_launches(int n) { g_last_launches = n; }
 static std::atomic<int> g_forward_schedule{MOK_SCHEDULE_TWO_LAUNCHES};
 
 int num_sms() {
@@ -75,7 +76,7 @@ static bool map3d(CUtensorMap* m, const void* p, uint64_t n, uint64_t rows, uint
 // ------------------------------------------------------------------ checks and layouts
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-static int check_dims(const mok_dims* d) {
+int check_dims(const mok_dims* d) {
   if (!d) return MOK_ERR_INVALID_ARG;
   if (d->T < 0 || d->T > 0x7fffffffLL / 8) return MOK_ERR_UNSUPPORTED;
   if (d->d <= 0 || d->d % 128) return MOK_ERR_UNSUPPORTED;
@@ -302,8 +303,8 @@ static int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOK_OK : MOK_E
 static int backward_mxfp8(const mok_dims* dims, const mok_weights* w, const void* x, const void* dY,
                           const void* saved, const int32_t* topk_idx, const float* topk_w,
                           const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
-                          const int32_t* inv_pos, void* dX, void* dW_gate, void* dW_up,
-                          void* dW_down, void* dWs_gate, void* dWs_up, void* dWs_down,
+                          const int32_t* inv_pos, const float* dlogits_aux, void* dX, void* dW_gate,
+                          void* dW_up, void* dW_down, void* dWs_gate, void* dWs_up, void* dWs_down,
                           float* dlogits, void* dW_router, void* ws, cudaStream_t s,
                           int* launches) {
   if (!w->prepared_bwd || !aligned16(w->prepared_bwd)) return MOK_ERR_INVALID_ARG;
@@ -382,7 +383,7 @@ static int backward_mxfp8(const mok_dims* dims, const mok_weights* w, const void
   }
   // 3. router backward: dw (128-column partials of <a, h>), dlogits, bf16 dl
   rc = cuda_status(launch_router_backward(T, E, k, F / 128, topk_idx, topk_w, inv_pos, part,
-                                          dlogits, W(BW_DL), s));
+                                          dlogits_aux, dlogits, W(BW_DL), s));
   if (rc != MOK_OK) return rc;
   ++*launches;
   // 4. dX_s = dG W_gate^T + dU W_up^T
@@ -767,10 +768,13 @@ int mok_dispatch_index(const mok_dims* dims, const int32_t* topk_idx, const floa
   return rc;
 }
 
-int mok_moe_forward(const mok_dims* dims, const mok_weights* w, const void* x,
-                    const int32_t* topk_idx, const int32_t* offsets, const int32_t* sorted_tok,
-                    const float* sorted_w, const int32_t* inv_pos, void* y, void* saved, void* ws,
-                    size_t ws_bytes, mok_stream_t stream) {
+// The forward of the expert part; with x_codes and x_scales (MXFP8 codes and scale atoms of x) the
+// MXFP8 path reads them instead of quantising x.
+static int moe_forward(const mok_dims* dims, const mok_weights* w, const void* x,
+                       const void* x_codes, const void* x_scales, const int32_t* topk_idx,
+                       const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
+                       const int32_t* inv_pos, void* y, void* saved, void* ws, size_t ws_bytes,
+                       mok_stream_t stream) {
   int rc = check_dims(dims);
   if (rc != MOK_OK) return rc;
   if (!w || !ws) return MOK_ERR_INVALID_ARG;
@@ -778,11 +782,11 @@ int mok_moe_forward(const mok_dims* dims, const mok_weights* w, const void* x,
     g_last_launches = 0;
     return ws_bytes < layout_fwd(dims).total ? MOK_ERR_WORKSPACE : MOK_OK;
   }
-  if (!y || !x || !topk_idx || !offsets || !sorted_tok || !sorted_w || !inv_pos)
+  if (!y || (!x && !x_codes) || !topk_idx || !offsets || !sorted_tok || !sorted_w || !inv_pos)
     return MOK_ERR_INVALID_ARG;
   if (!w->W_gate || !w->W_up || !w->W_down) return MOK_ERR_INVALID_ARG;
   if (dims->n_shared && (!w->Ws_gate || !w->Ws_up || !w->Ws_down)) return MOK_ERR_INVALID_ARG;
-  const void* ptrs[] = {x, y, saved, ws, w->W_gate, w->W_up, w->W_down, w->Ws_gate, w->Ws_up, w->Ws_down};
+  const void* ptrs[] = {x, x_codes, x_scales, y, saved, ws, w->W_gate, w->W_up, w->W_down, w->Ws_gate, w->Ws_up, w->Ws_down};
   for (const void* q : ptrs)
     if (q && !aligned16(q)) return MOK_ERR_UNSUPPORTED;
   const Layout L = layout_fwd(dims);
@@ -887,28 +891,30 @@ int mok_moe_forward(const mok_dims* dims, const mok_weights* w, const void* x,
   }
 
   if (dims->dtype == MOK_MXFP8) {
-    // MXFP8 path: x quantised once (E4M3 + UE8M0 per 32 along d), its codes and scale rows
-    // pulled into expert order, block-scaled gate/up GEMM whose epilogue quantises h along F,
+    // MXFP8 path: x quantised once (E4M3 + UE8M0 per 32 along d; or given so), its codes and
+    // scale rows pulled into expert order, block-scaled gate/up GEMM whose epilogue quantises h along F,
     // block-scaled down GEMM with the router weight, and the same bf16 combine.
     if (!w->prepared || !aligned16(w->prepared)) return MOK_ERR_INVALID_ARG;
     const Layout P = layout_prepared(dims);
     auto pw = [&](int i) { return static_cast<const char*>(w->prepared) + P.off[i]; };
-    void* xq = at<void*>(ws, L.off[FW_XQ]);
-    uint8_t* xsc = at<uint8_t*>(ws, L.off[FW_XSC]);
+    const void* xq = x_codes ? x_codes : at<void*>(ws, L.off[FW_XQ]);
+    const uint8_t* xsc = x_codes ? static_cast<const uint8_t*>(x_scales) : at<uint8_t*>(ws, L.off[FW_XSC]);
     void* xqs = at<void*>(ws, L.off[FW_XQS]);
     uint8_t* xscs = at<uint8_t*>(ws, L.off[FW_XSCS]);
     void* hq = at<void*>(ws, L.off[FW_HQ]);
     uint8_t* hsc = at<uint8_t*>(ws, L.off[FW_HSC]);
     void* hqsh = at<void*>(ws, L.off[FW_HQSH]);
     uint8_t* hscsh = at<uint8_t*>(ws, L.off[FW_HSCSH]);
-    rc = cuda_status(launch_mx_quantize_rows(x, T, d, xq, xsc, true, s));
+    if (!x_codes)
+      rc = cuda_status(launch_mx_quantize_rows(x, T, d, at<void*>(ws, L.off[FW_XQ]),
+                                               at<void*>(ws, L.off[FW_XSC]), true, s));
     if (rc == MOK_OK)
       rc = cuda_status(launch_gather_rows("gather_bytes", xq, nullptr, inv_pos, T, dims->k, d, xqs,
                                           nullptr, s));
     if (rc == MOK_OK)
       rc = cuda_status(launch_gather_scale_atoms(xsc, sorted_tok, offsets, E, T, R, d, xscs, s));
     if (rc != MOK_OK) return rc;
-    launches += 3;
+    launches += x_codes ? 2 : 3;
     {
       GemmParams p{};
       bool ok = true;
@@ -1134,12 +1140,44 @@ int mok_moe_forward(const mok_dims* dims, const mok_weights* w, const void* x,
   return MOK_OK;
 }
 
+int mok_moe_forward(const mok_dims* dims, const mok_weights* w, const void* x,
+                    const int32_t* topk_idx, const int32_t* offsets, const int32_t* sorted_tok,
+                    const float* sorted_w, const int32_t* inv_pos, void* y, void* saved, void* ws,
+                    size_t ws_bytes, mok_stream_t stream) {
+  return moe_forward(dims, w, x, nullptr, nullptr, topk_idx, offsets, sorted_tok, sorted_w, inv_pos,
+                     y, saved, ws, ws_bytes, stream);
+}
+
+int mok_moe_forward_mx(const mok_dims* dims, const mok_weights* w, const void* x_codes,
+                       const void* x_scales, const int32_t* topk_idx, const int32_t* offsets,
+                       const int32_t* sorted_tok, const float* sorted_w, const int32_t* inv_pos,
+                       void* y, void* saved, void* ws, size_t ws_bytes, mok_stream_t stream) {
+  const int rc = check_dims(dims);
+  if (rc != MOK_OK) return rc;
+  if (dims->dtype != MOK_MXFP8) return MOK_ERR_UNSUPPORTED;
+  if (dims->T > 0 && (!x_codes || !x_scales)) return MOK_ERR_INVALID_ARG;
+  return moe_forward(dims, w, nullptr, x_codes, x_scales, topk_idx, offsets, sorted_tok, sorted_w,
+                     inv_pos, y, saved, ws, ws_bytes, stream);
+}
+
 int mok_moe_backward(const mok_dims* dims, const mok_weights* w, const void* x, const void* dY,
                      const void* saved, const int32_t* topk_idx, const float* topk_w,
                      const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
                      const int32_t* inv_pos, void* dX, void* dW_gate, void* dW_up, void* dW_down,
                      void* dWs_gate, void* dWs_up, void* dWs_down, float* dlogits,
                      void* dW_router, void* ws, size_t ws_bytes, mok_stream_t stream) {
+  return mok_moe_backward_aux(dims, w, x, dY, saved, topk_idx, topk_w, offsets, sorted_tok, sorted_w,
+                              inv_pos, nullptr, dX, dW_gate, dW_up, dW_down, dWs_gate, dWs_up,
+                              dWs_down, dlogits, dW_router, ws, ws_bytes, stream);
+}
+
+int mok_moe_backward_aux(const mok_dims* dims, const mok_weights* w, const void* x, const void* dY,
+                         const void* saved, const int32_t* topk_idx, const float* topk_w,
+                         const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
+                         const int32_t* inv_pos, const float* dlogits_aux, void* dX, void* dW_gate,
+                         void* dW_up, void* dW_down, void* dWs_gate, void* dWs_up, void* dWs_down,
+                         float* dlogits, void* dW_router, void* ws, size_t ws_bytes,
+                         mok_stream_t stream) {
   int rc = check_dims(dims);
   if (rc != MOK_OK) return rc;
   if (dims->dtype == MOK_NVFP4) return MOK_ERR_UNSUPPORTED;  // the NVFP4 variant is forward only
@@ -1151,7 +1189,7 @@ int mok_moe_backward(const mok_dims* dims, const mok_weights* w, const void* x, 
   const bool sh = dims->n_shared == 1;
   if (sh && (!w->Ws_gate || !w->Ws_up || !w->Ws_down || !dWs_gate || !dWs_up || !dWs_down))
     return MOK_ERR_INVALID_ARG;
-  const void* ptrs[] = {x, dY, saved, ws, dX, dW_gate, dW_up, dW_down, dWs_gate, dWs_up, dWs_down,
+  const void* ptrs[] = {x, dY, saved, ws, dlogits_aux, dX, dW_gate, dW_up, dW_down, dWs_gate, dWs_up, dWs_down,
                         dW_router, w->W_router, w->W_gate, w->W_up, w->W_down, w->Ws_gate, w->Ws_up,
                         w->Ws_down};
   for (const void* q : ptrs)
@@ -1179,7 +1217,7 @@ int mok_moe_backward(const mok_dims* dims, const mok_weights* w, const void* x, 
     // the token-axis quantiser numbers its 128 x 64 tiles (x and dY) in an int
     if (2 * mx_nkb_routed(dims) * (d / 64) > 0x7fffffffLL) return MOK_ERR_UNSUPPORTED;
     rc = backward_mxfp8(dims, w, x, dY, saved, topk_idx, topk_w, offsets, sorted_tok, sorted_w,
-                        inv_pos, dX, dW_gate, dW_up, dW_down, dWs_gate, dWs_up, dWs_down, dlogits,
+                        inv_pos, dlogits_aux, dX, dW_gate, dW_up, dW_down, dWs_gate, dWs_up, dWs_down, dlogits,
                         dW_router, ws, s, &launches);
     if (rc == MOK_OK) g_last_launches = launches;
     return rc;
@@ -1242,7 +1280,7 @@ int mok_moe_backward(const mok_dims* dims, const mok_weights* w, const void* x, 
   }
   // 3. router backward: dw, dlogits, bf16 copy of dlogits
   rc = cuda_status(launch_router_backward(T, E, dims->k, F / bn_da, topk_idx, topk_w, inv_pos, P,
-                                          dlogits, dl, s));
+                                          dlogits_aux, dlogits, dl, s));
   if (rc != MOK_OK) return rc;
   ++launches;
   // 4. dX_s = dG W_gate^T + dU W_up^T; shared rows also take dl W_router^T

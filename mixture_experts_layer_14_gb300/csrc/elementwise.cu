@@ -183,12 +183,14 @@ cudaError_t launch_combine(int64_t T, int d, int k, const int32_t* topk_idx, con
 // Router backward for one token per warp.  dw_j = <dY_t, y_{e_j}(x_t)> is the fixed-order sum
 // of the per-N-tile partials <a, h> written by the down-projection backward epilogue; with
 // w_j = exp(l_j) / sum_{i in S} exp(l_i) (the renormalised softmax over the selection S),
-// dl_m = w_m (dw_m - sum_j w_j dw_j) for m in S and 0 elsewhere.  Writes dlogits[T,E] fp32 and
-// a bf16 copy dl[T,ldl] (columns E..ldl zero) that feeds the tensor-core GEMMs dl W_r^T, x^T dl.
+// dl_m = w_m (dw_m - sum_j w_j dw_j) for m in S and 0 elsewhere; aux[T,E] (or NULL), the gradient
+// of the router's own losses, is added in fp32.  Writes dlogits[T,E] fp32 and a bf16 copy
+// dl[T,ldl] (columns E..ldl zero) that feeds the tensor-core GEMMs dl W_r^T, x^T dl.
 __global__ void __launch_bounds__(kRowThreads) router_backward_kernel(
     int64_t T, int E, int k, int ldp, int ldl, const int32_t* __restrict__ topk_idx,
     const float* __restrict__ topk_w, const int32_t* __restrict__ inv_pos,
-    const float* __restrict__ partial, float* __restrict__ dlogits, __nv_bfloat16* __restrict__ dl) {
+    const float* __restrict__ partial, const float* __restrict__ aux, float* __restrict__ dlogits,
+    __nv_bfloat16* __restrict__ dl) {
   const int lane = threadIdx.x & 31;
   const int64_t wglobal = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
@@ -217,7 +219,10 @@ __global__ void __launch_bounds__(kRowThreads) router_backward_kernel(
         const float vj = __shfl_sync(0xffffffffu, dlj, j);
         if (ej == c) v = vj;
       }
-      if (c < E) dlogits[t * E + c] = v;
+      if (c < E) {
+        if (aux) v += aux[t * E + c];
+        dlogits[t * E + c] = v;
+      }
       dl[t * ldl + c] = __float2bfloat16_rn(v);
     }
   }
@@ -225,13 +230,13 @@ __global__ void __launch_bounds__(kRowThreads) router_backward_kernel(
 
 cudaError_t launch_router_backward(int64_t T, int E, int k, int ldp, const int32_t* topk_idx,
                                    const float* topk_w, const int32_t* inv_pos,
-                                   const float* partial, float* dlogits, void* dl_bf16,
-                                   cudaStream_t s) {
+                                   const float* partial, const float* aux, float* dlogits,
+                                   void* dl_bf16, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   const int ldl = (E + 63) & ~63;
   prof_begin("router_bwd", s);
   router_backward_kernel<<<rows_grid(T), kRowThreads, 0, s>>>(
-      T, E, k, ldp, ldl, topk_idx, topk_w, inv_pos, partial, dlogits,
+      T, E, k, ldp, ldl, topk_idx, topk_w, inv_pos, partial, aux, dlogits,
       static_cast<__nv_bfloat16*>(dl_bf16));
   prof_end(s);
   return cudaGetLastError();

@@ -176,10 +176,15 @@ cudaError_t launch_combine(int64_t T, int d, int k, const int32_t* topk_idx,
                            cudaStream_t s, const void* Ysh2 = nullptr);
 cudaError_t launch_router_backward(int64_t T, int E, int k, int ldp, const int32_t* topk_idx,
                                    const float* topk_w, const int32_t* inv_pos,
-                                   const float* partial, float* dlogits, void* dl_bf16,
-                                   cudaStream_t s);
+                                   const float* partial, const float* aux, float* dlogits,
+                                   void* dl_bf16, cudaStream_t s);
+
+// MOK_OK when the layer's sizes meet the preconditions of mok.h (api.cu).
+int check_dims(const mok_dims* d);
 
 int num_sms();
+// What mok_last_launch_count returns on this host thread.
+void set_last_launches(int n);
 
 // MXFP8 quantisation (mx.cu); scale atoms are described in mok_mx.cuh
 cudaError_t launch_mx_quantize_rows(const void* src, int64_t rows, int K, void* q, void* sc,

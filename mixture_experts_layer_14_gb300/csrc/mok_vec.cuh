@@ -1,0 +1,52 @@
+// Eight consecutive elements of a row, as the bandwidth-bound kernels around the layer hold them:
+// loads from and stores to bf16 (16 bytes) and fp32 (32 bytes), and sums over a warp.
+#pragma once
+
+#include "mok_device.cuh"
+
+namespace mok {
+
+struct Vec8 {
+  float v[8];
+};
+
+__device__ __forceinline__ Vec8 unpack8(uint4 u) {
+  return {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
+          bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
+}
+__device__ __forceinline__ uint4 pack8(const Vec8& a) {
+  return make_uint4(pack_bf16x2(a.v[0], a.v[1]), pack_bf16x2(a.v[2], a.v[3]),
+                    pack_bf16x2(a.v[4], a.v[5]), pack_bf16x2(a.v[6], a.v[7]));
+}
+// Vector `i` (elements 8 i ..) of a bf16 or fp32 array.
+template <bool F32>
+__device__ __forceinline__ Vec8 load8(const void* p, int64_t i) {
+  if constexpr (F32) {
+    const float4 a = static_cast<const float4*>(p)[2 * i], b = static_cast<const float4*>(p)[2 * i + 1];
+    return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  } else {
+    return unpack8(static_cast<const uint4*>(p)[i]);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t i, const Vec8& a) {
+  if constexpr (F32) {
+    static_cast<float4*>(p)[2 * i] = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
+    static_cast<float4*>(p)[2 * i + 1] = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
+  } else {
+    static_cast<uint4*>(p)[i] = pack8(a);
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+}  // namespace mok
