@@ -357,7 +357,7 @@ typedef struct {
  * all in fp32 on the master (or the fp32 param); a bf16 param is the rounded master.  `tensors`
  * is a HOST array, free for reuse when the call returns; clip is the device output of
  * mok_grad_norm: when its factor is NaN (a norm that is not finite) the step leaves everything
- * unchanged.  0 <= beta < 1, eps > 0, step >= 1. */
+ * unchanged.  0 <= beta < 1, eps >= 1e-15, step >= 1. */
 int mok_adamw_step(const mok_adamw_args *args, const mok_adamw_tensor *tensors, int n_tensors,
                    const float *clip, mok_stream_t stream);
 
