@@ -49,4 +49,20 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// Launches a kernel that may begin while the one before it in the stream still runs; it waits
+// with griddepcontrol.wait before it touches that one's results.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, int block, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3((unsigned)block);
+  c.stream = s;
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 }  // namespace mok
