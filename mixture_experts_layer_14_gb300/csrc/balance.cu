@@ -4,8 +4,9 @@
 // and n all of them, the balance loss is a sum over tokens once c is known:
 //   balance = sum_t a_s <c_s, p_t>,  a_s = alpha E / (k n n_s),  s = the token's sequence,
 //   dl_t = p_t (a_s (c_s - <c_s, p_t>) + b lse_t),  b = 2 z_coef / n,
-// so one pass over the logits gives loss and gradient.  Counts are integer atomics (any order
-// gives the same sums); the losses are summed per block and joined in a fixed order.
+// so one pass over the logits gives loss and gradient.  Two launches: the counts (integers, in
+// shared memory, one thread-block cluster per sequence), then that pass, whose blocks start while
+// the counts are taken and whose last block joins the blocks' losses in a fixed order.
 #include <algorithm>
 #include <cmath>
 
@@ -14,7 +15,10 @@
 namespace mok {
 
 constexpr int kBalThreads = 256;
-constexpr int kBalMaxBlocks = 2048;
+constexpr int kBalMaxBlocks = 1024;
+constexpr int kBalBlocksPerSm = 3;
+constexpr int kCountThreads = 512;
+constexpr int kCountCluster = 8;
 
 struct BalanceParams {
   const float* logits;
@@ -23,136 +27,293 @@ struct BalanceParams {
   const uint8_t* mask;         // or NULL
   const float* grad;           // or NULL
   int32_t* counts;             // [S, E]
-  int32_t* n_seq;              // [S], then the total
+  int32_t* n_seq;              // [S], then the ticket of the pass's blocks
   float2* partial;             // [blocks] {sum a <c, p>, sum lse^2}
   float* loss;
   float* dlogits;              // or NULL
   int* status;
   int64_t T;
-  int S, E, k, blocks;
+  int S, E, k;
+  uint32_t inv_k;              // ceil(2^32 / k)
   float alpha, z_coef;
 };
 
-// Sequence of token t, or -1 when it is left out.
-__device__ __forceinline__ int sequence_of(const BalanceParams& p, int64_t t) {
-  if (p.mask && !p.mask[t]) return -1;
-  if (!p.seq_offsets) return 0;
-  int lo = 0, hi = p.S + 1;  // the first entry above t is in [lo, hi]
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.seq_offsets[mid] <= t) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo - 1 < p.S ? lo - 1 : -1;
+// First token of sequence s (s = S: the end of the last one), within [0, T].
+__device__ __forceinline__ int64_t sequence_begin(const BalanceParams& p, int s) {
+  if (!p.seq_offsets) return s ? p.T : 0;
+  return min(max((int64_t)p.seq_offsets[s], (int64_t)0), p.T);
 }
 
-__global__ void __launch_bounds__(kBalThreads) balance_count_kernel(const __grid_constant__ BalanceParams p) {
-  for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < p.T; t += (int64_t)gridDim.x * blockDim.x) {
-    const int s = sequence_of(p, t);
-    if (s < 0) continue;
-    atomicAdd(p.n_seq + s, 1);
-    atomicAdd(p.n_seq + p.S, 1);
-    for (int j = 0; j < p.k; ++j) {
-      const int e = p.topk_idx[t * p.k + j];
-      if (e < 0 || e >= p.E) record_status(p.status, MOK_ERR_DEVICE_CHECK);
-      else atomicAdd(p.counts + (int64_t)s * p.E + e, 1);
+// One cluster (or, for many sequences, one block) per sequence; rank r of C takes every C-th batch
+// of its routes.  Every rank counts in its own shared memory, then adds up a C-th of the experts
+// over all ranks.  At T = 16384, k = 8, E = 384 it is bound by the latency of reading 64 KB of
+// routes per block and of two cluster barriers.
+__global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __grid_constant__ BalanceParams p, int C) {
+  __shared__ int hist[kMaxE + 1];  // the last one: valid tokens
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int s = blockIdx.x / C, rank = C > 1 ? (int)cluster_ctarank() : 0;
+  for (int e = threadIdx.x; e <= p.E; e += kCountThreads) hist[e] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.n_seq[p.S] = 0;
+  __syncthreads();
+  const int64_t first = sequence_begin(p, s) * p.k, end = sequence_begin(p, s + 1) * p.k;
+  constexpr int kBatch = 4;
+  for (int64_t r = first + (int64_t)rank * kBatch * kCountThreads + threadIdx.x; r < end;
+       r += (int64_t)C * kBatch * kCountThreads) {
+    int e[kBatch];
+    bool valid[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const uint32_t q = (uint32_t)(r + i * kCountThreads);  // routes are numbered below 2^31
+      valid[i] = r + i * kCountThreads < end;
+      e[i] = valid[i] ? p.topk_idx[q] : 0;
+      if (valid[i] && p.mask) {
+        uint32_t t = p.k == 1 ? q : __umulhi(q, p.inv_k);  // q / k, or one more
+        t -= t * p.k > q;
+        valid[i] = p.mask[t] != 0;
+        if (valid[i] && t * p.k == q) atomicAdd(&hist[p.E], 1);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (!valid[i]) continue;
+      if ((uint32_t)e[i] < (uint32_t)p.E) atomicAdd(&hist[e[i]], 1);
+      else record_status(p.status, MOK_ERR_DEVICE_CHECK);
     }
   }
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+  const int per = (p.E + 1 + C - 1) / C;
+  for (int e = rank * per + threadIdx.x; e < min(p.E + 1, (rank + 1) * per); e += kCountThreads) {
+    int n = 0;
+    if (C > 1) {
+      for (int q = 0; q < C; ++q) {
+        int v;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(&hist[e]), (uint32_t)q)));
+        n += v;
+      }
+    } else {
+      n = hist[e];
+    }
+    if (e < p.E) p.counts[(int64_t)s * p.E + e] = n;
+    else p.n_seq[s] = p.mask ? n : (int)max((end - first) / p.k, (int64_t)0);
+  }
+  if (C > 1) cluster_sync();  // the others read this block's counts until here
 }
 
-// One warp per token; lane i holds the 4-element vectors i, i + 32, ... of its logits.
-__global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const __grid_constant__ BalanceParams p) {
-  __shared__ float2 smem[kBalThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int nvec = p.E / 4;
-  const float n = (float)max(p.n_seq[p.S], 1);
+// Sequence of token t, or -1; a warp searches 32 of the S + 1 offsets at a time.
+__device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_t t, int lane) {
+  if (!offsets) return 0;
+  int lo = 0, hi = S + 1;  // the first offset above t is in [lo, hi]
+  while (hi - lo > 32) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = min(lo + (lane + 1) * step - 1, hi - 1);
+    const int below = __popc(__ballot_sync(0xffffffffu, offsets[at] <= t));
+    lo = min(lo + below * step, hi);
+    hi = min(lo + step, hi);
+  }
+  lo += __popc(__ballot_sync(0xffffffffu, lo + lane < hi && offsets[min(lo + lane, S)] <= t));
+  return lo - 1 < S ? lo - 1 : -1;
+}
+// The offsets in shared memory, where they fit; the block synchronises before it reads them.
+constexpr int kOffsets = 1024;
+__device__ __forceinline__ const int32_t* near_offsets(const BalanceParams& p, int32_t* smem, int threads) {
+  if (!p.seq_offsets || p.S >= kOffsets) return p.seq_offsets;
+  for (int i = threadIdx.x; i <= p.S; i += threads) smem[i] = p.seq_offsets[i];
+  return smem;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Losses and gradients of the tokens [t, end) of a warp (neighbours, so that the counts of their
+// sequence stay in registers); the warp's {sum a <c, p>, sum lse^2}, the same in all lanes.  Lane i holds the 4-element vectors i, i + 32, ... of a
+// token's logits (EV of them); the next kRing tokens' come into a ring in shared memory by
+// asynchronous copies, each lane's to where it reads them back itself.  exp(l - max) is
+// 2^(l log2 e - m) with one rounding of the exponent; m is the same for the whole row, so that its
+// own rounding cancels in the softmax and enters lse once.
+// ready() comes before the first use of counts and n_seq and returns the number of valid tokens;
+// sequence(t, s) is the sequence of a token, or -1, s the one of a token before it, or -1.
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int ring_of(int ev) { return ev == 4 ? 2 : 3; }  // rows; at most 36 KB per block
+template <int EV, class Ready, class Sequence>
+__device__ __forceinline__ float2 balance_tokens(const BalanceParams& p, int64_t t, int64_t end, uint32_t ring,
+                                                 Ready ready, Sequence sequence, float* inv_n_out) {
+  constexpr int kRing = ring_of(EV);
+  const int lane = threadIdx.x & 31, nvec = p.E / 4;
+  ring += 16 * lane;
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < end) {
+      const float4* src = reinterpret_cast<const float4*>(p.logits) + row * nvec + lane;
+#pragma unroll
+      for (int i = 0; i < EV; ++i)
+        if (lane + 32 * i < nvec) copy16(ring + (slot * EV + i) * 512, src + 32 * i);
+    }
+    copies_end();
+  };
+  auto mask = [&](int64_t row) { return row < end && p.mask ? (uint32_t)p.mask[row] : 1u; };
+#pragma unroll
+  for (int k = 0; k < kRing; ++k) fetch(t + k, k);
+  uint32_t mask_now = mask(t), mask_next = mask(t + 1);
+  const float inv_n = 1.0f / (float)max(ready(), 1);
+  *inv_n_out = inv_n;
   const float g = p.grad ? *p.grad : 1.0f;
-  float sum_b = 0.0f, sum_z = 0.0f;
-  for (int64_t t = (int64_t)blockIdx.x * (kBalThreads / 32) + warp; t < p.T; t += (int64_t)gridDim.x * (kBalThreads / 32)) {
-    const int s = sequence_of(p, t);
-    float4 l[kMaxE / 128], c[kMaxE / 128];
+  const float a_all = p.alpha * (float)p.E / (float)p.k * inv_n, b_all = 2.0f * p.z_coef * inv_n;
+  float2 sum = make_float2(0.0f, 0.0f);
+  float2 c[2 * EV];
+  float a = 0.0f;
+  int s_held = -1, slot = 0;
+  for (; t < end; ++t) {
+    const int s = mask_now ? sequence(t, s_held) : -1;
+    mask_now = mask_next;
+    mask_next = mask(t + 2);
+    float2 l[2 * EV];
     float top = -INFINITY;
-    if (s >= 0) {
+    copies_wait<kRing - 1>();
 #pragma unroll
-      for (int i = 0; i < kMaxE / 128; ++i) {
-        const int v = lane + 32 * i;
-        if (v < nvec) {
-          l[i] = reinterpret_cast<const float4*>(p.logits)[t * nvec + v];
-          const int4 ci = reinterpret_cast<const int4*>(p.counts)[(int64_t)s * nvec + v];
-          c[i] = make_float4((float)ci.x, (float)ci.y, (float)ci.z, (float)ci.w);
-        } else {
-          l[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-          c[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-        top = fmaxf(top, fmaxf(fmaxf(l[i].x, l[i].y), fmaxf(l[i].z, l[i].w)));
+    for (int i = 0; i < EV; ++i) {
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (lane + 32 * i < nvec) v = ld_shared_v4(ring + (slot * EV + i) * 512);
+      l[2 * i] = make_float2(v.x, v.y);
+      l[2 * i + 1] = make_float2(v.z, v.w);
+      top = fmaxf(top, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+    }
+    fetch(t + kRing, slot);  // this place is in registers now
+    slot = slot + 1 == kRing ? 0 : slot + 1;
+    if (s != s_held && s >= 0) {
+      s_held = s;
+      a = a_all / (float)p.n_seq[s];
+      const int4* src = reinterpret_cast<const int4*>(p.counts) + (int64_t)s * nvec + lane;
+#pragma unroll
+      for (int i = 0; i < EV; ++i) {
+        const int4 ci = lane + 32 * i < nvec ? src[32 * i] : make_int4(0, 0, 0, 0);
+        c[2 * i] = make_float2((float)ci.x, (float)ci.y);
+        c[2 * i + 1] = make_float2((float)ci.z, (float)ci.w);
       }
     }
-    top = warp_max(top);
-    const float base = top == -INFINITY ? 0.0f : top;
-    float total = 0.0f, inner = 0.0f;
-    if (s >= 0) {
-#pragma unroll
-      for (int i = 0; i < kMaxE / 128; ++i) {
-        l[i] = make_float4(expf(l[i].x - base), expf(l[i].y - base), expf(l[i].z - base), expf(l[i].w - base));
-        total += (l[i].x + l[i].y) + (l[i].z + l[i].w);
-        inner = fmaf(c[i].x, l[i].x, fmaf(c[i].y, l[i].y, fmaf(c[i].z, l[i].z, fmaf(c[i].w, l[i].w, inner))));
-      }
-    }
-    total = warp_sum(total);
-    inner = warp_sum(inner);
-    const bool live = s >= 0 && total != 0.0f;  // a NaN total stays live
-    float a = 0.0f, b = 0.0f, inv = 0.0f;
+    bool live = s >= 0;
+    float q = 0.0f, inner = 0.0f, b = 0.0f;
     if (live) {
-      inv = 1.0f / total;
-      inner *= inv;
-      a = p.alpha * (float)p.E / ((float)p.k * n * (float)p.n_seq[s]);
-      const float lse = base + logf(total);
-      b = 2.0f * p.z_coef / n * lse;
-      sum_b += a * inner;
-      sum_z += lse * lse;
+      top = warp_max(top);
+      const float m = top == -INFINITY ? 0.0f : top * kLog2e;
+      float2 total2 = make_float2(0.0f, 0.0f), inner2 = total2;
+#pragma unroll
+      for (int i = 0; i < 2 * EV; ++i) {
+        const float2 x = __ffma2_rn(l[i], make_float2(kLog2e, kLog2e), make_float2(-m, -m));
+        l[i] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+        total2 = __fadd2_rn(total2, l[i]);
+        inner2 = __ffma2_rn(c[i], l[i], inner2);
+      }
+      float2 r = make_float2(total2.x + total2.y, inner2.x + inner2.y);
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+        r = __fadd2_rn(r, make_float2(__shfl_xor_sync(0xffffffffu, r.x, o), __shfl_xor_sync(0xffffffffu, r.y, o)));
+      live = r.x != 0.0f;  // nothing but -inf: no loss, no gradient (a NaN total stays live)
+      if (live) {
+        const float inv = 1.0f / r.x, lse = m * kLn2 + logf(r.x);
+        inner = r.y * inv;
+        b = b_all * lse;
+        sum.x += a * inner;
+        sum.y += lse * lse;
+        q = g * inv;
+      }
     }
     if (p.dlogits) {
+      float4* dst = reinterpret_cast<float4*>(p.dlogits) + t * nvec + lane;
+      const float2 q2 = make_float2(q, q), a2 = make_float2(a, a), b2 = make_float2(b, b), i2 = make_float2(-inner, -inner);
 #pragma unroll
-      for (int i = 0; i < kMaxE / 128; ++i) {
-        const int v = lane + 32 * i;
-        if (v < nvec) {
-          float4 d = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int i = 0; i < EV; ++i) {
+        if (lane + 32 * i < nvec) {
+          float2 lo = make_float2(0.0f, 0.0f), hi = lo;
           if (live) {
-            const float q = g * inv;
-            d = make_float4(l[i].x * q * (a * (c[i].x - inner) + b), l[i].y * q * (a * (c[i].y - inner) + b),
-                            l[i].z * q * (a * (c[i].z - inner) + b), l[i].w * q * (a * (c[i].w - inner) + b));
+            lo = __fmul2_rn(__fmul2_rn(l[2 * i], q2), __ffma2_rn(a2, __fadd2_rn(c[2 * i], i2), b2));
+            hi = __fmul2_rn(__fmul2_rn(l[2 * i + 1], q2), __ffma2_rn(a2, __fadd2_rn(c[2 * i + 1], i2), b2));
           }
-          reinterpret_cast<float4*>(p.dlogits)[t * nvec + v] = d;
+          dst[32 * i] = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
       }
     }
   }
-  if (lane == 0) smem[warp] = make_float2(sum_b, sum_z);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float2 a = make_float2(0.0f, 0.0f);
-    for (int w = 0; w < kBalThreads / 32; ++w) {
-      a.x += smem[w].x;
-      a.y += smem[w].y;
-    }
-    p.partial[blockIdx.x] = a;
-  }
+  return sum;
 }
 
-__global__ void __launch_bounds__(32) balance_loss_kernel(const __grid_constant__ BalanceParams p) {
-  double b = 0.0, z = 0.0;
-  for (int i = threadIdx.x; i < p.blocks; i += 32) {
-    b += p.partial[i].x;
-    z += p.partial[i].y;
+// Sum over the block's warps, in order; in thread 0.
+__device__ __forceinline__ float2 block_join(float2 v, float2* smem, int warps) {
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
+  __syncthreads();
+  for (int w = 1; w < warps && threadIdx.x == 0; ++w) {
+    v.x += smem[w].x;
+    v.y += smem[w].y;
   }
-  for (int o = 16; o; o >>= 1) {
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-  }
+  return v;
+}
+__device__ __forceinline__ void write_loss(const BalanceParams& p, float2 v, float inv_n) {
+  p.loss[0] = v.x;
+  p.loss[1] = v.y * p.z_coef * inv_n;
+}
+
+// Valid tokens of all sequences (every thread of the block calls this).
+__device__ __forceinline__ int valid_tokens(const BalanceParams& p, const int32_t* n_seq, int* smem, int threads) {
+  if (!p.mask) return (int)max(sequence_begin(p, p.S) - sequence_begin(p, 0), (int64_t)0);
+  int own = 0;
+  for (int s = threadIdx.x; s < p.S; s += threads) own += n_seq[s];
+  own = __reduce_add_sync(0xffffffffu, own);
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = own;
+  __syncthreads();
+  int n = 0;
+  for (int w = 0; w < threads / 32; ++w) n += smem[w];
+  return n;
+}
+
+// At T = 16384, E = 384, k = 8 (50.9 MB): 15.4 us with the counts, of 7.5 at the copy rate; at
+// T = 65536 47 us of 30.  About 5 us go to the counts and the start; the pass itself waits on the
+// chain of a token's two reductions, exponentials and logarithm (380 instructions per token, half
+// of the issue slots with 24 warps per SM).  Tokens strided over the warps 17 us (the counts of a
+// sequence are read again for every token), four blocks per SM 15.9, five 17.9.
+template <int EV>
+__global__ void __launch_bounds__(kBalThreads, kBalBlocksPerSm) balance_grad_kernel(const __grid_constant__ BalanceParams p) {
+  constexpr int kWarps = kBalThreads / 32;
+  __shared__ float2 smem[kWarps];
+  __shared__ int total[kWarps];
+  __shared__ int32_t own_offsets[kOffsets];
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31;
+  float inv_n;
+  extern __shared__ __align__(16) uint8_t ring[];
+  const int32_t* offsets = nullptr;
+  auto ready = [&]() {
+    offsets = near_offsets(p, own_offsets, kBalThreads);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are there
+    __syncthreads();
+    return valid_tokens(p, p.n_seq, total, kBalThreads);
+  };
+  const int64_t per = (p.T + (int64_t)gridDim.x * kWarps - 1) / ((int64_t)gridDim.x * kWarps);
+  const int64_t first = per * ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5));
+  float2 v = balance_tokens<EV>(p, first, min(first + per, p.T), smem_u32(ring) + (threadIdx.x >> 5) * (ring_of(EV) * EV * 512), ready,
+                                [&](int64_t t, int s) {
+                                  if (s >= 0 && (!offsets || t < offsets[s + 1])) return s;
+                                  return sequence_of(offsets, p.S, t, lane);
+                                },
+                                &inv_n);
+  v = block_join(v, smem, kWarps);
   if (threadIdx.x == 0) {
-    p.loss[0] = (float)b;
-    p.loss[1] = (float)(z * (double)p.z_coef / (double)max(p.n_seq[p.S], 1));
+    p.partial[blockIdx.x] = v;
+    __threadfence();
+    last = atomicAdd(p.n_seq + p.S, 1) == (int)gridDim.x - 1;
   }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  v = make_float2(0.0f, 0.0f);
+  for (int i = threadIdx.x; i < gridDim.x; i += kBalThreads) {
+    const float2 u = __ldcg(p.partial + i);
+    v.x += u.x;
+    v.y += u.y;
+  }
+  v = block_join(make_float2(warp_sum(v.x), warp_sum(v.y)), smem, kWarps);
+  if (threadIdx.x == 0) write_loss(p, v, inv_n);
 }
 
 static size_t balance_ws(int64_t S) {
@@ -202,24 +363,43 @@ int mok_balance_loss(const mok_dims* dims, const float* logits, const int32_t* t
   p.S = (int)n_seqs;
   p.E = dims->E;
   p.k = dims->k;
+  p.inv_k = (uint32_t)((0x100000000ull + p.k - 1) / p.k);
   p.alpha = alpha;
   p.z_coef = z_coef;
-  const int64_t warps = kBalThreads / 32;
-  p.blocks = (int)std::max<int64_t>(1, std::min<int64_t>((p.T + warps - 1) / warps, std::min(kBalMaxBlocks, num_sms() * 8)));
-  cudaError_t e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * n_seqs * p.E, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(p.n_seq, 0, sizeof(int32_t) * (n_seqs + 1), s);
-  if (e != cudaSuccess) return MOK_ERR_CUDA;
+  const int ev = (p.E + 127) / 128;
+  auto pick = [&](auto one, auto two, auto three, auto four) { return ev == 1 ? one : ev == 2 ? two : ev == 3 ? three : four; };
+  // counts: a cluster per sequence when sequences are long and their clusters fill the GPU about
+  // four times at most
+  cudaError_t e;
   prof_begin("balance_count", s);
-  balance_count_kernel<<<(int)std::max<int64_t>(1, std::min<int64_t>((p.T + kBalThreads - 1) / kBalThreads, num_sms() * 8)), kBalThreads, 0, s>>>(p);
+  if (n_seqs * kCountCluster <= 4LL * num_sms() && p.T * p.k > n_seqs * 4 * kCountThreads) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    cfg.gridDim = dim3((unsigned)(n_seqs * kCountCluster));
+    cfg.blockDim = dim3(kCountThreads);
+    cfg.stream = s;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kCountCluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, balance_count_kernel, p, kCountCluster);
+  } else {
+    balance_count_kernel<<<(unsigned)n_seqs, kCountThreads, 0, s>>>(p, 1);
+    e = cudaGetLastError();
+  }
   prof_end(s);
+  if (e != cudaSuccess) return MOK_ERR_CUDA;
+  // as many blocks as are resident together, and no more of them than give every warp its tokens
+  const int64_t warps = kBalThreads / 32, most = std::min(kBalMaxBlocks, num_sms() * kBalBlocksPerSm);
+  const int64_t turns = std::max<int64_t>(1, (p.T + warps * most - 1) / (warps * most));
+  const int blocks = (int)std::max<int64_t>(1, (p.T + warps * turns - 1) / (warps * turns));
   prof_begin("balance_grad", s);
-  balance_grad_kernel<<<p.blocks, kBalThreads, 0, s>>>(p);
+  e = launch_after_smem(kBalThreads / 32 * ring_of(ev) * ev * 512, pick(balance_grad_kernel<1>, balance_grad_kernel<2>, balance_grad_kernel<3>, balance_grad_kernel<4>),
+                   blocks, kBalThreads, s, p);
   prof_end(s);
-  prof_begin("balance_loss", s);
-  balance_loss_kernel<<<1, 32, 0, s>>>(p);
-  prof_end(s);
-  if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
-  set_last_launches(3);
+  if (e != cudaSuccess) return MOK_ERR_CUDA;
+  set_last_launches(2);
   return MOK_OK;
 }
 

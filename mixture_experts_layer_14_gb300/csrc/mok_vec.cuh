@@ -38,6 +38,21 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const Vec8& a) {
   }
 }
 
+// Asynchronous 16-byte copies to shared memory, in groups; copies_wait<N> waits until all but this
+// thread's newest N groups have landed (it sees only its own: a thread that reads back exactly
+// what it copied needs no barrier).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_ca(uint32_t dst, const void* src) {  // through L1
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -52,10 +67,11 @@ __device__ __forceinline__ float warp_max(float v) {
 // Launches a kernel that may begin while the one before it in the stream still runs; it waits
 // with griddepcontrol.wait before it touches that one's results.
 template <class... P, class... A>
-cudaError_t launch_after(void (*kernel)(P...), int grid, int block, cudaStream_t s, A... args) {
+cudaError_t launch_after_smem(int smem, void (*kernel)(P...), int grid, int block, cudaStream_t s, A... args) {
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)grid);
   c.blockDim = dim3((unsigned)block);
+  c.dynamicSmemBytes = (size_t)smem;
   c.stream = s;
   cudaLaunchAttribute a = {};
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -63,6 +79,10 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int block, cudaStream_t
   c.attrs = &a;
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, kernel, args...);
+}
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, int block, cudaStream_t s, A... args) {
+  return launch_after_smem(0, kernel, grid, block, s, args...);
 }
 
 }  // namespace mok

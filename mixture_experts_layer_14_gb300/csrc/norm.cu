@@ -80,19 +80,12 @@ __device__ __forceinline__ Vec8 value8(const Raw8<F32>& r) {
     return unpack8(r.u[0]);
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_ca(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until all but the newest n groups of this thread's copies have landed, n <= 2.
 __device__ __forceinline__ void copies_wait(int n) {
   switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 0: copies_wait<0>(); break;
+    case 1: copies_wait<1>(); break;
+    default: copies_wait<2>(); break;
   }
 }
 
@@ -285,8 +278,8 @@ __global__ void __launch_bounds__(MT) rms_norm_bwd_kernel(const __grid_constant_
   };
   auto landed = [&]() {  // all but the newest row (with two places: all)
     if constexpr (RING) {
-      if (deep) asm volatile("cp.async.wait_group 1;" ::: "memory");
-      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (deep) copies_wait<1>();
+      else copies_wait<0>();
     }
   };
   auto read = [&](int64_t row, uint32_t at, int v, Pairs* s, Pairs* dy) {
