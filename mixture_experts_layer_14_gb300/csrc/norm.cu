@@ -80,24 +80,17 @@ __device__ __forceinline__ Vec8 value8(const Raw8<F32>& r) {
     return unpack8(r.u[0]);
 }
 
-// Waits until all but the newest n groups of this thread's copies have landed, n <= 2.
-__device__ __forceinline__ void copies_wait(int n) {
-  switch (n) {
-    case 0: copies_wait<0>(); break;
-    case 1: copies_wait<1>(); break;
-    default: copies_wait<2>(); break;
-  }
-}
-
-// Vector v of a row (vector i of the array) to the ring's place `at` (bytes): bf16 in one plane of
-// 16 bytes per vector, fp32 in two (through L1: each copy uses half a sector).
+// Vector v of a row that begins at vector `row` of the array, to the ring's place `at` (bytes): bf16
+// in one plane of 16 bytes per vector; fp32 in two, through L1, because each copy uses half a
+// sector (past L1, or with the halves of a warp's vectors redistributed, 10-25% slower).
 template <bool F32>
-__device__ __forceinline__ void copy8(uint32_t at, const void* p, int64_t i, int v, int nvec) {
+__device__ __forceinline__ void copy8(uint32_t at, const void* p, int64_t row, int v, int nvec) {
+  if (v >= nvec) return;
   if constexpr (F32) {
-    copy16_ca(at + 16 * v, static_cast<const uint4*>(p) + 2 * i);
-    copy16_ca(at + 16 * (nvec + v), static_cast<const uint4*>(p) + 2 * i + 1);
+    copy16_ca(at + 16 * v, static_cast<const uint4*>(p) + 2 * (row + v));
+    copy16_ca(at + 16 * (nvec + v), static_cast<const uint4*>(p) + 2 * (row + v) + 1);
   } else {
-    copy16(at + 16 * v, static_cast<const uint4*>(p) + i);
+    copy16(at + 16 * v, static_cast<const uint4*>(p) + row + v);
   }
 }
 __device__ __forceinline__ uint4 ring16(uint32_t at) {
@@ -118,8 +111,8 @@ __device__ __forceinline__ Vec8 load_weight(const void* w, int f32, int v, bool 
 }
 
 // RES: 0 no residual, 1 bf16, 2 fp32.  V vectors per thread, MT threads at most.  At T = 16384,
-// d = 7168 with a bf16 residual and MXFP8 output (1.06 GB) 157 us, 6.7 TB/s; one row in the ring
-// instead of three 175 us, a block per row without a ring 229 us.
+// d = 7168 with a bf16 residual and MXFP8 output (1.06 GB) 156 us, 6.8 TB/s; a block per row without
+// a ring 229 us.
 template <int V, int RES, int MT>
 __global__ void __launch_bounds__(MT) rms_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float2 smem[2][32];
@@ -130,18 +123,17 @@ __global__ void __launch_bounds__(MT) rms_norm_kernel(const __grid_constant__ No
   constexpr int kPlanes = 1 + (RES == 0 ? 0 : RES);  // of 16 bytes per vector
   const uint32_t place = kPlanes * 16 * nvec;        // bytes of a row
   const uint32_t base = smem_u32(ring) + threadIdx.y * p.depth * place;
+  constexpr bool kHold = V < 4;  // the weight in registers; else read where it is used, from L1 or L2
   bool in[V];
-  Vec8 w[V];
+  Vec8 w[kHold ? V : 1];
   auto fetch = [&](int64_t row, int slot) {
     if (row < p.T) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
-        if (in[i]) {
-          const uint32_t at = base + slot * place;
-          copy8<false>(at, p.x, row * nvec + v, v, nvec);
-          if constexpr (RES != 0) copy8<RES == 2>(at + 16 * nvec, p.residual, row * nvec + v, v, nvec);
-        }
+        const uint32_t at = base + slot * place;
+        copy8<false>(at, p.x, row * nvec, v, nvec);
+        if constexpr (RES != 0) copy8<RES == 2>(at + 16 * nvec, p.residual, row * nvec, v, nvec);
       }
     }
     copies_end();
@@ -150,12 +142,13 @@ __global__ void __launch_bounds__(MT) rms_norm_kernel(const __grid_constant__ No
   for (int i = 0; i < V; ++i) in[i] = threadIdx.x + i * blockDim.x < nvec;
   for (int k = 0; k < p.depth; ++k) fetch(t + k * step, k);
 #pragma unroll
-  for (int i = 0; i < V; ++i) w[i] = load_weight(p.weight, p.weight_f32, threadIdx.x + i * blockDim.x, in[i]);
+  for (int i = 0; i < (kHold ? V : 0); ++i) w[i] = load_weight(p.weight, p.weight_f32, threadIdx.x + i * blockDim.x, in[i]);
   int slot = 0;
   for (int turn = 0; t < p.T; t += step, turn ^= 1) {
     Vec8 h[V];
     float ss = 0.0f;
-    copies_wait(p.depth - 1);
+    if (p.depth == 2) copies_wait<1>();
+    else copies_wait<0>();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -177,8 +170,9 @@ __global__ void __launch_bounds__(MT) rms_norm_kernel(const __grid_constant__ No
     for (int i = 0; i < V; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (RES != 0 && in[i]) store8<RES == 2>(p.residual_out, t * nvec + v, h[i]);
+      const Vec8 g = kHold ? w[kHold ? i : 0] : load_weight(p.weight, p.weight_f32, v, in[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[i].v[j] = h[i].v[j] * rho * w[i].v[j];
+      for (int j = 0; j < 8; ++j) h[i].v[j] = h[i].v[j] * rho * g.v[j];
       if (p.y && in[i]) store8<false>(p.y, t * nvec + v, h[i]);
       if (p.codes) {
         float amax = 0.0f;
@@ -252,8 +246,12 @@ __global__ void __launch_bounds__(MT) rms_norm_bwd_kernel(const __grid_constant_
   const int nvec = p.d >> 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t row_step = (int64_t)gridDim.x * nvec;  // vectors from a turn's row to the next one's
   const int64_t end = p.T * nvec;
+  constexpr bool kHold = V < 4;  // the weight in registers; else read where it is used, from L1 or L2
   bool in[V];
-  Pairs dw[V], w[V];
+  Pairs dw[V], w[kHold ? V : 1];
+  auto weight = [&](int i) {
+    return kHold ? w[kHold ? i : 0] : pairs(load_weight(p.weight, p.weight_f32, threadIdx.x + i * blockDim.x, true));
+  };
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kPlanes = F32 ? 2 : 1;  // of 16 bytes per vector: one for dy, then s, then dres
   const uint32_t s_at = 16 * nvec, r_at = s_at + 16 * kPlanes * nvec;
@@ -267,11 +265,9 @@ __global__ void __launch_bounds__(MT) rms_norm_bwd_kernel(const __grid_constant_
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
-        if (in[i]) {
-          copy8<false>(at, p.dy, row + v, v, nvec);
-          copy8<F32>(at + s_at, p.s, row + v, v, nvec);
-          if (DRES && p.ring_res) copy8<F32>(at + r_at, p.dres, row + v, v, nvec);
-        }
+        copy8<false>(at, p.dy, row, v, nvec);
+        copy8<F32>(at + s_at, p.s, row, v, nvec);
+        if (DRES && p.ring_res) copy8<F32>(at + r_at, p.dres, row, v, nvec);
       }
     }
     copies_end();
@@ -298,11 +294,12 @@ __global__ void __launch_bounds__(MT) rms_norm_bwd_kernel(const __grid_constant_
     for (int i = 0; i < V; ++i) {
       if (in[i]) {
         Pairs a, b;
+        const Pairs g = weight(i);
         read(row, at, threadIdx.x + i * blockDim.x, &a, &b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           ss = __ffma2_rn(a.p[j], a.p[j], ss);
-          dot = __ffma2_rn(a.p[j], __fmul2_rn(b.p[j], w[i].p[j]), dot);
+          dot = __ffma2_rn(a.p[j], __fmul2_rn(b.p[j], g.p[j]), dot);
         }
       }
     }
@@ -319,7 +316,7 @@ __global__ void __launch_bounds__(MT) rms_norm_bwd_kernel(const __grid_constant_
   fetch(row, base);
   if (deep) fetch(row + row_step, base + place);
 #pragma unroll
-  for (int i = 0; i < V; ++i) w[i] = pairs(load_weight(p.weight, p.weight_f32, threadIdx.x + i * blockDim.x, in[i]));
+  for (int i = 0; i < (kHold ? V : 0); ++i) w[i] = pairs(load_weight(p.weight, p.weight_f32, threadIdx.x + i * blockDim.x, in[i]));
   landed();
   {
     const float2 own = sums_of(row, base);
@@ -331,6 +328,8 @@ __global__ void __launch_bounds__(MT) rms_norm_bwd_kernel(const __grid_constant_
     fetch(row + (deep ? 2 : 1) * row_step, last);
     landed();
     const uint32_t next = at + place == base + p.depth * place ? base : at + place;
+    Raw8<F32> res = zero8<F32>();  // dres, if not in the ring: early where registers allow
+    if (DRES && V == 1 && in[0] && !(RING && p.ring_res)) res = raw8<F32>(p.dres, row + threadIdx.x);
     float2 own = both(0.0f), sums = lane < warps ? smem[turn][lane] : both(0.0f);
     if (row + row_step < end) own = sums_of(row + row_step, next);
 #pragma unroll
@@ -349,12 +348,15 @@ __global__ void __launch_bounds__(MT) rms_norm_bwd_kernel(const __grid_constant_
         read(row, at, v, &a, &b);
         Vec8 ds;
         Pairs r;
+        const Pairs gw = weight(i);
         if constexpr (DRES)
-          r = pairs(value8<F32>(RING && p.ring_res ? ring8<F32>(at + r_at, v, nvec) : raw8<F32>(p.dres, row + v)));
+          r = pairs(value8<F32>(RING && p.ring_res ? ring8<F32>(at + r_at, v, nvec)
+                                   : V == 1                ? res
+                                                           : raw8<F32>(p.dres, row + v)));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           dw[i].p[j] = __ffma2_rn(b.p[j], __fmul2_rn(a.p[j], rho2), dw[i].p[j]);
-          const float2 g = __ffma2_rn(a.p[j], c, __fmul2_rn(b.p[j], w[i].p[j]));
+          const float2 g = __ffma2_rn(a.p[j], c, __fmul2_rn(b.p[j], gw.p[j]));
           const float2 q = DRES ? __ffma2_rn(g, rho2, r.p[j]) : __fmul2_rn(g, rho2);
           ds.v[2 * j] = q.x;
           ds.v[2 * j + 1] = q.y;
@@ -430,13 +432,17 @@ static bool norm_sizes_ok(int64_t T, int d) {
 }
 // Vectors per thread (1, 2 or 4), threads of a row, rows of a block, blocks per SM and the ring's
 // depth.  One vector per thread up to 1024 threads: at T = 16384, d = 7168 with MXFP8 output 160 us
-// against 168 us with two (448 threads); blocks fill an SM's registers with 1024 threads.
+// against 168 us with two (448 threads); blocks fill an SM's registers with 1024 threads.  More
+// rows under way than the copies' latency needs cost bandwidth: forward, 2^26 elements, with one /
+// two / three rows per block 84 / 93 / 96 us at d = 4096 (two blocks per SM, bf16; 79 at the copy
+// rate) and 90 / 85 / 93 at d = 7168 (one).
 struct NormShape {
   int v, threads, rows, blocks, depth;
 };
-constexpr int kSmemPerSm = 227 * 1024;                // for the blocks of an SM together
-constexpr int kSmemOwn = 2048;                        // of a block: reserved and static
-constexpr int kRingBytes = kSmemPerSm - kSmemOwn;     // most dynamic bytes of a block
+constexpr int kSmemPerSm = 227 * 1024;             // for the blocks of an SM together
+constexpr int kSmemOwn = 2048;                     // of a block: reserved and static
+constexpr int kRingBytes = kSmemPerSm - kSmemOwn;  // most dynamic bytes of a block
+constexpr int kPlainSmem = 40 * 1024;              // dynamic bytes that need no attribute
 static NormShape norm_shape(int64_t T, int d, int row_bytes, bool warp_rows) {
   NormShape n;
   const int nvec = d / 8;
@@ -445,17 +451,17 @@ static NormShape norm_shape(int64_t T, int d, int row_bytes, bool warp_rows) {
   n.rows = warp_rows && n.threads == 32 ? 8 : 1;
   n.blocks = std::max(1, std::min(1024 / (n.threads * n.rows), 8));
   const int64_t turns = (T + (int64_t)num_sms() * n.blocks * n.rows - 1) / ((int64_t)num_sms() * n.blocks * n.rows);
-  n.depth = std::min(3, (kSmemPerSm / n.blocks - kSmemOwn) / (n.rows * row_bytes));
-  n.depth = (int)std::max<int64_t>(1, std::min<int64_t>(n.depth, turns));
+  n.depth = n.blocks > 1 || turns < 2 || 2 * row_bytes > kRingBytes ? 1 : 2;
   return n;
 }
-// Backward: two rows at least, or depth 0 where they do not fit; dres goes through the ring where
-// three rows with it fit.
+// Backward: two rows at least, three where they fit, or depth 0 where not even two do.  dres goes
+// through the ring in bf16 where three rows with it fit; in fp32 it comes straight to registers
+// (2^26 elements at d = 7168: 165 us against 198 through the ring, 158 at the copy rate).
 static NormShape norm_bwd_shape(int64_t T, int d, bool f32, bool dres, int* row_bytes, int* ring_res) {
   const int plane = 2 * d, planes = f32 ? 2 : 1;
   NormShape n = norm_shape(T, d, plane, false);
   const int room = kSmemPerSm / n.blocks - kSmemOwn;
-  *ring_res = dres && 3 * plane * (1 + 2 * planes) <= room;
+  *ring_res = dres && !f32 && 9 * plane <= room;
   *row_bytes = plane * (1 + planes * (*ring_res ? 2 : 1));
   n.depth = std::min(3, room / *row_bytes);
   const int64_t turns = (T + (int64_t)num_sms() * n.blocks - 1) / ((int64_t)num_sms() * n.blocks);
@@ -506,7 +512,7 @@ int mok_rms_norm(int64_t T, int d, float eps, const void* x, const void* residua
   else if (res_type == MOK_T_BF16) pick(std::integral_constant<int, 1>{});
   else pick(std::integral_constant<int, 2>{});
   const int smem = n.depth * n.rows * row_bytes;
-  if (smem > 48 * 1024 && cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
+  if (smem > kPlainSmem && cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
     return MOK_ERR_CUDA;
   prof_begin("rms_norm", s);
   k<<<grid, dim3(n.threads, n.rows), smem, s>>>(p);
@@ -557,7 +563,7 @@ int mok_rms_norm_backward(int64_t T, int d, float eps, const void* dy, const voi
   else if (dres) pick(std::false_type{}, std::true_type{});
   else pick(std::false_type{}, std::false_type{});
   const int smem = n.depth * row_bytes;
-  if (smem > 48 * 1024 && cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
+  if (smem > kPlainSmem && cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
     return MOK_ERR_CUDA;
   prof_begin("rms_norm_bwd", st);
   k<<<grid, n.threads, smem, st>>>(p);

@@ -6,13 +6,16 @@ and two products v is within 80 u of its value.  A bf16 output is the rounding o
 lies between the roundings of the two ends of that interval.
 """
 
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import mixture_experts_layer_14_gb300 as mok
 from tests import _around as plain
-from tests._helpers import ensure_lib, f64
+from tests._helpers import ROOT, ensure_lib, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -181,6 +184,34 @@ def test_zero_rows_and_non_finite_rows():
     g = mok.rms_norm_backward(torch.empty((0, 256), dtype=torch.bfloat16, device="cuda"),
                               torch.empty((0, 256), dtype=torch.float32, device="cuda"), w.cuda(), EPS)
     assert (g["dweight"] == 0).all()
+
+
+WIDTHS = """
+import torch
+import mixture_experts_layer_14_gb300 as mok
+T = 330
+for d in [*range(8, 600, 72), *range(1024, 5400, 152), *range(5440, 17000, 992), 24000, 32760]:
+    x = torch.randn(T, d, device="cuda").bfloat16()
+    w = torch.ones(d, device="cuda")
+    for kind in (None, torch.bfloat16, torch.float32):
+        r = None if kind is None else torch.randn(T, d, device="cuda").to(kind)
+        h = x.float() if r is None else x.float() + r.float()
+        y = h * torch.rsqrt(h.square().mean(1, keepdim=True) + 1e-6)
+        out = mok.rms_norm(x, w, 1e-6, residual=r)
+        assert (out["y"].float() - y).abs().max() <= 2 ** -7 * y.abs().max(), (d, kind)
+        s = out.get("residual", x)
+        g = mok.rms_norm_backward(x, s, w, 1e-6, dres=None if r is None else s)
+        assert g["dx"].isfinite().all() and g["dweight"].isfinite().all(), (d, kind)
+torch.cuda.synchronize()
+"""
+
+
+def test_every_width_in_a_fresh_process():
+    """Shared-memory sizes on both sides of what a launch gets unasked: each kernel's first launch in
+    the process is with the smaller ones."""
+    ensure_lib()
+    r = subprocess.run([sys.executable, "-c", WIDTHS], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_offsets_beyond_32_bits():
