@@ -174,6 +174,11 @@ def _want(t, name, shape, dtype, device, check_device=True):
     return t
 
 
+def _want_ws(ws, device):
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+
+
 def dims(T, d, E, k, F, F_shared=0, n_shared=1, dtype=MOK_BF16):
     return Dims(T, d, E, k, F, F_shared if n_shared else 0, n_shared, dtype)
 
@@ -405,6 +410,7 @@ def rms_norm_backward(dy, s, weight, eps=1e-6, dres=None, ws=None):
         _want(dres, "dres", (T, d), s.dtype, dev)
     if ws is None:
         ws = torch.empty(rms_norm_workspace_size(T, d), dtype=torch.uint8, device=dev)
+    _want_ws(ws, dev)
     out = {"dx": torch.empty_like(dy), "dweight": torch.empty((d,), dtype=torch.float32, device=dev)}
     if st:
         out["dresidual"] = torch.empty_like(s)
@@ -441,6 +447,7 @@ def balance_loss(D, logits, topk_idx, ws, alpha, z_coef=0.0, seq_offsets=None, t
         _want(token_mask, "token_mask", (D.T,), torch.bool, dev)
     if grad is not None:
         _want(grad, "grad", (1,), torch.float32, dev)
+    _want_ws(ws, dev)
     out = {"loss": torch.empty((2,), dtype=torch.float32, device=dev),
            "counts": torch.empty((S, D.E), dtype=torch.int32, device=dev)}
     if want_dlogits:

@@ -147,8 +147,11 @@ __global__ void __launch_bounds__(256) grad_norm_join_kernel(const float* __rest
 }
 
 // ------------------------------------------------------------------ AdamW
-constexpr int kAdamChunk = 4096;    // elements per block, fp32 states
-constexpr int kAdamChunkMx = 8192;  // and 8-bit ones
+constexpr int kAdamTurn = 8 * kOptThreads;  // elements of a block per turn
+constexpr int kAdamTurns = 2;               // turns of a chunk, fp32 states
+constexpr int kAdamTurnsMx = 4;             // and 8-bit ones
+template <bool MX>
+constexpr int kAdamChunk = (MX ? kAdamTurnsMx : kAdamTurns) * kAdamTurn;
 constexpr int kAdamCap = 384;     // tensors per launch: about 30 KB of the 32 KB of parameters
 constexpr int kAdamCapSmall = 24;
 
@@ -298,8 +301,8 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int n, uint2 c) 
 template <bool P32, bool G32>
 __device__ __forceinline__ void adam_chunk_f32(const AdamEntry& t, const AdamHyper& h, float clip, int64_t at) {
 #pragma unroll 1
-  for (int u = 0; u < kAdamChunk; u += 8 * kOptThreads) {
-    const int64_t i = at + u + 8 * threadIdx.x;
+  for (int u = 0; u < kAdamTurns; ++u) {
+    const int64_t i = at + u * kAdamTurn + 8 * threadIdx.x;
     const int n = (int)min((int64_t)8, t.numel - i);
     if (n <= 0) return;
     const Vec8 g = load8n<G32>(t.grad, i, n);
@@ -326,11 +329,10 @@ struct AdamRaw {
 // arithmetic, which alone takes about half of the issue slots.
 template <bool P32, bool G32, bool FULL>
 __device__ __forceinline__ void adam_chunk_mx(const AdamEntry& t, const AdamHyper& h, float clip, int64_t at) {
-  constexpr int kTurns = kAdamChunkMx / (8 * kOptThreads);
   void* const wp = P32 ? t.param : t.master;
   AdamRaw<G32> raw[2];
   auto load = [&](int u, AdamRaw<G32>& r) {
-    const int64_t i = at + u * (8 * kOptThreads) + 8 * threadIdx.x;
+    const int64_t i = at + u * kAdamTurn + 8 * threadIdx.x;
     if constexpr (G32) {
       r.g[0] = static_cast<const uint4*>(t.grad)[i >> 2];
       r.g[1] = static_cast<const uint4*>(t.grad)[(i >> 2) + 1];
@@ -345,13 +347,14 @@ __device__ __forceinline__ void adam_chunk_mx(const AdamEntry& t, const AdamHype
     r.vs = t.vs[i >> 5];
   };
   if constexpr (FULL) load(0, raw[0]);
-#pragma unroll
-  for (int u = 0; u < kTurns; ++u) {
-    const int64_t i = at + u * (8 * kOptThreads) + 8 * threadIdx.x;
+#pragma unroll(FULL ? kAdamTurnsMx : 1)
+  for (int u = 0; u < kAdamTurnsMx; ++u) {
+    if (!FULL && at + u * kAdamTurn >= t.numel) break;
+    const int64_t i = at + u * kAdamTurn + 8 * threadIdx.x;
     Vec8 g, w, m, v;
     int n = 8;
     if constexpr (FULL) {
-      if (u + 1 < kTurns) load(u + 1, raw[(u + 1) & 1]);
+      if (u + 1 < kAdamTurnsMx) load(u + 1, raw[(u + 1) & 1]);
       const AdamRaw<G32>& r = raw[u & 1];
       if constexpr (G32) {
         const uint4 a = r.g[0], b = r.g[1];
@@ -397,7 +400,7 @@ __device__ __forceinline__ void adam_chunk_mx(const AdamEntry& t, const AdamHype
 template <bool MX, bool P32, bool G32>
 __device__ __forceinline__ void adam_chunk(const AdamEntry& t, const AdamHyper& h, float clip, int64_t at) {
   if constexpr (!MX) adam_chunk_f32<P32, G32>(t, h, clip, at);
-  else if (at + kAdamChunkMx <= t.numel) adam_chunk_mx<P32, G32, true>(t, h, clip, at);
+  else if (at + kAdamChunk<true> <= t.numel) adam_chunk_mx<P32, G32, true>(t, h, clip, at);
   else adam_chunk_mx<P32, G32, false>(t, h, clip, at);
 }
 
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kOptThreads, MX ? 4 : 1) adamw_kernel(const __
   if (clip != clip) return;  // the gradients' norm is not finite: nothing changes
   const int k = tensor_of(p, blockIdx.x);
   const AdamEntry& t = p.t[k];
-  const int64_t at = (int64_t)(blockIdx.x - (k ? p.end[k - 1] : 0u)) * (MX ? kAdamChunkMx : kAdamChunk);
+  const int64_t at = (int64_t)(blockIdx.x - (k ? p.end[k - 1] : 0u)) * kAdamChunk<MX>;
   if (t.param_f32) {
     if (t.grad_f32) adam_chunk<MX, true, true>(t, p.h, clip, at);
     else adam_chunk<MX, true, false>(t, p.h, clip, at);
@@ -474,13 +477,14 @@ static cudaError_t launch_adam(int n, const mok_adamw_tensor* t, const AdamHyper
   p.h = h;
   p.clip = clip;
   for (int j = 0; j < n; ++j) {
-    c += chunks_of(t[j].numel, MX ? kAdamChunkMx : kAdamChunk);
+    c += chunks_of(t[j].numel, kAdamChunk<MX>);
     p.t[j] = AdamEntry{t[j].param, t[j].grad, t[j].master, t[j].exp_avg, t[j].exp_avg_sq, t[j].exp_avg_scale,
                        t[j].exp_avg_sq_scale, t[j].numel, (float)t[j].weight_decay, t[j].param_type == MOK_T_F32,
                        t[j].grad_type == MOK_T_F32};
     p.end[j] = (uint32_t)c;
   }
   if (c == 0) return cudaSuccess;
+  if (c > 0x7fffffffLL) return cudaErrorInvalidValue;
   prof_begin("adamw", s);
   adamw_kernel<CAP, MX><<<(unsigned)c, kOptThreads, 0, s>>>(p);
   prof_end(s);

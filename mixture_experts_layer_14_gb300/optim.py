@@ -9,7 +9,7 @@ import ctypes
 import numpy as np
 import torch
 
-from . import (AdamWArgs, AdamWTensor, MokError, _check, _elem, _ptr, _stream, lib)
+from . import _ELEM, AdamWArgs, AdamWTensor, MokError, _check, _elem, _ptr, _stream, _want_ws, lib
 
 __all__ = ["TensorList", "grad_norm", "grad_norm_workspace_size", "AdamW"]
 
@@ -31,20 +31,22 @@ class TensorList:
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
-        for i, t in enumerate(self.tensors):
-            _elem(t, f"tensor {i}")
-            if not t.is_contiguous():
-                raise ValueError(f"tensor {i} must be contiguous")
-            if not t.is_cuda or t.device != self.tensors[0].device:
-                raise ValueError(f"tensor {i} must live on one CUDA device with the others")
         n = len(self.tensors)
         self.device = self.tensors[0].device if n else torch.device("cuda", torch.cuda.current_device())
-        self.pointers = (ctypes.c_void_p * n)(*[t.data_ptr() or None for t in self.tensors])
-        self.numel = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
-        self.types = (ctypes.c_int32 * n)(*[_elem(t, "tensor") for t in self.tensors])
-        self.view_pointers, self.view_numel, self.view_types = (
-            np.frombuffer(a, dtype=k) if n else np.zeros(0, dtype=k)
-            for a, k in ((self.pointers, np.uint64), (self.numel, np.int64), (self.types, np.int32)))
+        types = [_ELEM.get(t.dtype, -1) for t in self.tensors]
+        for i, t in enumerate(self.tensors):
+            if types[i] < 0:
+                _elem(t, f"tensor {i}")
+            if not t.is_contiguous():
+                raise ValueError(f"tensor {i} must be contiguous")
+            if not t.is_cuda or t.device != self.device:
+                raise ValueError(f"tensor {i} must live on one CUDA device with the others")
+        self.view_pointers = np.array([t.data_ptr() for t in self.tensors], dtype=np.uint64)
+        self.view_numel = np.array([t.numel() for t in self.tensors], dtype=np.int64)
+        self.view_types = np.array(types, dtype=np.int32)
+        # the same arrays as C pointers
+        self.pointers, self.numel, self.types = (
+            a.ctypes.data for a in (self.view_pointers, self.view_numel, self.view_types))
 
     def __len__(self):
         return len(self.tensors)
@@ -70,6 +72,7 @@ def grad_norm(grads, max_norm=0.0, ws=None):
     g = _as_list(grads)
     if ws is None:
         ws = torch.empty(grad_norm_workspace_size(g), dtype=torch.uint8, device=g.device)
+    _want_ws(ws, g.device)
     out = torch.empty(2, dtype=torch.float32, device=g.device)
     _check(lib().mok_grad_norm(len(g), g.pointers, g.numel, g.types, max_norm, _ptr(out), _ptr(ws),
                                ws.numel(), _stream()))
@@ -77,9 +80,11 @@ def grad_norm(grads, max_norm=0.0, ws=None):
 
 
 class AdamW:
-    """AdamW over a list of weights, one launch per step (up to 384 tensors).
+    """AdamW over a list of weights, one launch per step (up to 384 tensors; more take several).
 
-    ``params``: bf16 or fp32 CUDA tensors, updated in place.  A bf16 weight has an fp32 master that
+    ``params``: bf16 or fp32 CUDA tensors, updated in place (held, with their addresses: they must
+    not be given other storage).  The learning rate and the step's number are constants of the
+    launch, in a captured CUDA graph too.  A bf16 weight has an fp32 master that
     the steps accumulate in.  ``states``: "f32", or "mxfp8" for E4M3 codes with one power-of-two
     scale per 32 elements and dithered rounding (1.03 bytes per state and element; mok.h,
     mok_state_format).  ``weight_decay``: one value, or one per tensor.  ``state``: buffers to use
@@ -149,21 +154,20 @@ class AdamW:
             raise ValueError(f"{len(g)} gradients for {len(self.params)} tensors")
         if not np.array_equal(self._view["numel"], g.view_numel):
             i = int(np.nonzero(self._view["numel"] != g.view_numel)[0][0])
-            raise ValueError(f"gradient {i}: {g.numel[i]} elements, the weight has {self.params[i].numel()}")
+            raise ValueError(f"gradient {i}: {g.view_numel[i]} elements, the weight has {self.params[i].numel()}")
         if len(g) and g.device != self.device:
             raise ValueError(f"gradients must live on {self.device}")
         self._view["grad"], self._view["grad_type"] = g.view_pointers, g.view_types
         if clip is not None and (clip.dtype != torch.float32 or clip.numel() != 2 or clip.device != self.device
                                  or not clip.is_contiguous()):
             raise ValueError(f"clip must be 2 fp32 values on {self.device}")
-        self.args.lr = lr
-        self.args.step += 1
-        try:
-            _check(lib().mok_adamw_step(ctypes.byref(self.args), self.table, len(self.params), _ptr(clip),
-                                        _stream()))
-        except MokError:
-            self.args.step -= 1
-            raise
+        args = self.args
+        args.lr = lr
+        args.step += 1
+        rc = lib().mok_adamw_step(ctypes.byref(args), self.table, len(self.params), _ptr(clip), _stream())
+        if rc != 0:
+            args.step -= 1
+            _check(rc)
 
     def state_dict(self):
         """The states (not copied) and the number of steps: AdamW(params, ..., **state_dict()) goes on

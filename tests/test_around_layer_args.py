@@ -138,6 +138,10 @@ def test_binding_checks():
         mok.TensorList([x.half()])
     with pytest.raises(ValueError):
         mok.AdamW([], states="int4")
+    with pytest.raises(ValueError):
+        mok._want_ws(torch.zeros(8, dtype=torch.uint8), torch.device("cpu"))
+    with pytest.raises(ValueError):
+        mok._want_ws(torch.zeros(8), torch.device("cpu"))
     D = mok.dims(4, 128, 8, 2, 128, 0, 0)
     with pytest.raises(ValueError):
         mok.balance_loss(D, torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int64), torch.zeros(8), 0.1)

@@ -135,6 +135,33 @@ def test_index_out_of_range_is_reported():
     assert (out["counts"].cpu().numpy() == counts).all()
 
 
+def test_no_tokens():
+    ensure_lib()
+    out, status = _run(torch.empty((0, 16)), torch.empty((0, 2), dtype=torch.int32), 0.02, 1e-3)
+    assert status == 0 and (out["loss"] == 0).all() and (out["counts"] == 0).all() and out["dlogits"].shape == (0, 16)
+
+
+def test_on_the_layers_own_workspace_and_in_a_graph():
+    """The layer's forward workspace will do; a captured graph replays the two launches."""
+    ensure_lib()
+    logits, idx = _inputs(700, 64, 4, 11)
+    D = mok.dims(700, 128, 64, 4, 128, 0, 0)
+    ws = torch.zeros(mok.workspace_size(D), dtype=torch.uint8, device="cuda")
+    want, _ = _run(logits, idx, 0.02, 1e-3)
+    lc, ic = logits.cuda(), idx.cuda()
+    got = mok.balance_loss(D, lc, ic, ws, 0.02, z_coef=1e-3)
+    assert all(torch.equal(want[key], got[key]) for key in want) and mok.read_status(ws) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = mok.balance_loss(D, lc, ic, ws, 0.02, z_coef=1e-3)
+    for _ in range(3):
+        for t in got.values():
+            t.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(want[key], got[key]) for key in want)
+
+
 def test_upstream_gradient_and_no_gradient():
     ensure_lib()
     logits, idx = _inputs(90, 16, 2, 6)

@@ -198,6 +198,52 @@ def test_adamw_skips_a_step_without_a_finite_norm(states):
     assert all(torch.equal(a, b) for a, b in zip(before, after))
 
 
+def test_adamw_refusals():
+    ensure_lib()
+    params, grads, _ = _weights([100, 33])
+    opt = mok.AdamW(params, states="mxfp8")
+    for bad in (grads[:1], [grads[0], grads[1][:32]], [grads[0], grads[1].half()], [grads[0].cpu(), grads[1]]):
+        with pytest.raises(ValueError):
+            opt.step(bad, 1e-3)
+    with pytest.raises(ValueError):
+        opt.step(grads, 1e-3, clip=torch.ones(1, device="cuda"))
+    with pytest.raises(mok.MokError):
+        opt.step(grads, float("nan"))
+    assert opt.steps == 0
+    state = opt.state_dict()["state"]
+    for key, value in (("exp_avg", state["exp_avg"][:1]), ("exp_avg_sq", [state["exp_avg_sq"][0].float()] * 2),
+                       ("exp_avg_scale", [None, None])):
+        with pytest.raises(ValueError):
+            mok.AdamW(params, states="mxfp8", state=dict(state, **{key: value}))
+    with pytest.raises(ValueError):
+        mok.AdamW(params, weight_decay=[0.1])
+    with pytest.raises(ValueError):
+        mok.TensorList([grads[0], torch.ones((4, 4), device="cuda").t()])
+    with pytest.raises(ValueError):
+        mok.grad_norm(grads, 1.0, ws=torch.zeros(4096, device="cuda"))
+    with pytest.raises(mok.MokError):
+        mok.grad_norm(grads, 1.0, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(mok.MokError):       # not 16-byte aligned
+        mok.grad_norm([torch.ones(9, device="cuda")[1:]], 1.0)
+
+
+def test_side_stream():
+    """Both on a stream of their own, waiting for the inputs there."""
+    ensure_lib()
+    params, grads, _ = _weights([5000, 77])
+    other = [p.clone() for p in params]
+    opt, twin = mok.AdamW(params), mok.AdamW(other)
+    clip = mok.grad_norm(grads, 0.1)
+    opt.step(grads, 1e-2, clip=clip)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = mok.grad_norm(grads, 0.1)
+        twin.step(grads, 1e-2, clip=again)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(clip, again) and all(torch.equal(p, q) for p, q in zip(params, other))
+
+
 def test_adamw_beyond_32_bits():
     """More than 2^31 elements (17 GB on the device): the last ones get the step of a small tensor."""
     ensure_lib()
