@@ -18,7 +18,6 @@ constexpr int kBalThreads = 256;
 constexpr int kBalMaxBlocks = 1024;
 constexpr int kBalBlocksPerSm = 3;
 constexpr int kCountThreads = 512;
-constexpr int kCountCluster = 8;
 
 struct BalanceParams {
   const float* logits;
@@ -34,7 +33,6 @@ struct BalanceParams {
   int* status;
   int64_t T;
   int S, E, k;
-  uint32_t inv_k;              // ceil(2^32 / k)
   float alpha, z_coef;
 };
 
@@ -44,42 +42,71 @@ __device__ __forceinline__ int64_t sequence_begin(const BalanceParams& p, int s)
   return min(max((int64_t)p.seq_offsets[s], (int64_t)0), p.T);
 }
 
-// One cluster (or, for many sequences, one block) per sequence; rank r of C takes every C-th batch
-// of its routes.  Every rank counts in its own shared memory, then adds up a C-th of the experts
-// over all ranks.  At T = 16384, k = 8, E = 384 it is bound by the latency of reading 64 KB of
-// routes per block and of two cluster barriers.
+// The k experts of a token.  VEC: k is 4 or 8 and the rows are 16-byte aligned.
+template <bool VEC>
+__device__ __forceinline__ void load_routes(const BalanceParams& p, int64_t t, int (&e)[kMaxK]) {
+#pragma unroll
+  for (int j = 0; j < kMaxK; j += 4) {
+    if constexpr (VEC) {
+      if (j < p.k) {
+        const int4 q = *reinterpret_cast<const int4*>(p.topk_idx + t * p.k + j);
+        e[j] = q.x;
+        e[j + 1] = q.y;
+        e[j + 2] = q.z;
+        e[j + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = j; i < j + 4; ++i)
+        if (i < p.k) e[i] = p.topk_idx[t * p.k + i];
+    }
+  }
+}
+
+// One cluster of C blocks (C = 1: one block) per sequence; a thread takes a token at a time, two
+// under way.  Every rank counts in its own shared memory, then adds up a C-th of the experts over
+// all ranks.  Bound by latency: of the routes' loads, of shared-memory additions to the experts
+// that many tokens choose, and of two cluster barriers.  The whole call at T = 16384, E = 384, k = 8
+// with one sequence takes 30 / 21 / 16.5 / 14.3 us with C = 1 / 2 / 4 / 8, with 37 sequences 16.1 /
+// 14.8 / 14.4 / 15.1, with 200 14.2 / 15.5 / 18.7 / 25.8; a thread per route instead of per token
+// 16.1 us (one sequence, C = 8), 22 with a mask.
+template <bool VEC>
 __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __grid_constant__ BalanceParams p, int C) {
   __shared__ int hist[kMaxE + 1];  // the last one: valid tokens
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int s = blockIdx.x / C, rank = C > 1 ? (int)cluster_ctarank() : 0;
   for (int e = threadIdx.x; e <= p.E; e += kCountThreads) hist[e] = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) p.n_seq[p.S] = 0;
+  const int64_t first = sequence_begin(p, s), end = sequence_begin(p, s + 1);
   __syncthreads();
-  const int64_t first = sequence_begin(p, s) * p.k, end = sequence_begin(p, s + 1) * p.k;
-  constexpr int kBatch = 4;
-  for (int64_t r = first + (int64_t)rank * kBatch * kCountThreads + threadIdx.x; r < end;
-       r += (int64_t)C * kBatch * kCountThreads) {
-    int e[kBatch];
-    bool valid[kBatch];
+  const int64_t step = (int64_t)C * kCountThreads;
+  int own = 0;
+  for (int64_t t = first + (int64_t)rank * kCountThreads + threadIdx.x; t < end; t += 2 * step) {
+    int e[2][kMaxK];
+    bool valid[2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const uint32_t q = (uint32_t)(r + i * kCountThreads);  // routes are numbered below 2^31
-      valid[i] = r + i * kCountThreads < end;
-      e[i] = valid[i] ? p.topk_idx[q] : 0;
-      if (valid[i] && p.mask) {
-        uint32_t t = p.k == 1 ? q : __umulhi(q, p.inv_k);  // q / k, or one more
-        t -= t * p.k > q;
-        valid[i] = p.mask[t] != 0;
-        if (valid[i] && t * p.k == q) atomicAdd(&hist[p.E], 1);
+    for (int i = 0; i < 2; ++i) {
+      const int64_t at = t + i * step;
+      valid[i] = at < end;
+      if (valid[i]) {
+        load_routes<VEC>(p, at, e[i]);
+        if (p.mask) valid[i] = p.mask[at] != 0;
       }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if (!valid[i]) continue;
-      if ((uint32_t)e[i] < (uint32_t)p.E) atomicAdd(&hist[e[i]], 1);
-      else record_status(p.status, MOK_ERR_DEVICE_CHECK);
+      ++own;
+#pragma unroll
+      for (int j = 0; j < kMaxK; ++j) {
+        if (j >= p.k) continue;
+        if ((uint32_t)e[i][j] < (uint32_t)p.E) atomicAdd(&hist[e[i][j]], 1);
+        else record_status(p.status, MOK_ERR_DEVICE_CHECK);
+      }
     }
   }
+  own = __reduce_add_sync(0xffffffffu, own);
+  if ((threadIdx.x & 31) == 0 && own) atomicAdd(&hist[p.E], own);
   if (C > 1) cluster_sync();
   else __syncthreads();
   const int per = (p.E + 1 + C - 1) / C;
@@ -95,7 +122,7 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __gr
       n = hist[e];
     }
     if (e < p.E) p.counts[(int64_t)s * p.E + e] = n;
-    else p.n_seq[s] = p.mask ? n : (int)max((end - first) / p.k, (int64_t)0);
+    else p.n_seq[s] = n;
   }
   if (C > 1) cluster_sync();  // the others read this block's counts until here
 }
@@ -267,11 +294,12 @@ __device__ __forceinline__ int valid_tokens(const BalanceParams& p, const int32_
   return n;
 }
 
-// At T = 16384, E = 384, k = 8 (50.9 MB): 15.4 us with the counts, of 7.5 at the copy rate; at
-// T = 65536 47 us of 30.  About 5 us go to the counts and the start; the pass itself waits on the
-// chain of a token's two reductions, exponentials and logarithm (380 instructions per token, half
-// of the issue slots with 24 warps per SM).  Tokens strided over the warps 17 us (the counts of a
-// sequence are read again for every token), four blocks per SM 15.9, five 17.9.
+// At T = 16384, E = 384, k = 8, 37 sequences (50.9 MB): 14.4 us with the counts, of 7.5 at the copy
+// rate; at T = 65536 42 us of 30.  About 5 us go to the counts and the start; the pass itself (35 us
+// at T = 65536, 5.8 TB/s) waits on the chain of a token's two reductions, exponentials and
+// logarithm (380 instructions per token, 55% of the issue slots with 24 warps per SM).  Tokens
+// strided over the warps cost 1.5 us more (the counts of a sequence are read again for every
+// token), four blocks per SM 0.5, five 2.5.
 template <int EV>
 __global__ void __launch_bounds__(kBalThreads, kBalBlocksPerSm) balance_grad_kernel(const __grid_constant__ BalanceParams p) {
   constexpr int kWarps = kBalThreads / 32;
@@ -363,29 +391,31 @@ int mok_balance_loss(const mok_dims* dims, const float* logits, const int32_t* t
   p.S = (int)n_seqs;
   p.E = dims->E;
   p.k = dims->k;
-  p.inv_k = (uint32_t)((0x100000000ull + p.k - 1) / p.k);
   p.alpha = alpha;
   p.z_coef = z_coef;
   const int ev = (p.E + 127) / 128;
   auto pick = [&](auto one, auto two, auto three, auto four) { return ev == 1 ? one : ev == 2 ? two : ev == 3 ? three : four; };
-  // counts: a cluster per sequence when sequences are long and their clusters fill the GPU about
-  // four times at most
+  // blocks of a sequence's cluster: a power of two up to 8 that leaves each about 100 tokens
+  int C = 1;
+  while (C < 8 && 2 * C * 96 * n_seqs <= p.T) C *= 2;
+  const bool vec = p.k % 4 == 0 && (reinterpret_cast<uintptr_t>(topk_idx) & 15u) == 0;
+  const auto count = vec ? balance_count_kernel<true> : balance_count_kernel<false>;
   cudaError_t e;
   prof_begin("balance_count", s);
-  if (n_seqs * kCountCluster <= 4LL * num_sms() && p.T * p.k > n_seqs * 4 * kCountThreads) {
+  if (C > 1) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = {};
-    cfg.gridDim = dim3((unsigned)(n_seqs * kCountCluster));
+    cfg.gridDim = dim3((unsigned)(n_seqs * C));
     cfg.blockDim = dim3(kCountThreads);
     cfg.stream = s;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = kCountCluster;
+    attr.val.clusterDim.x = C;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, balance_count_kernel, p, kCountCluster);
+    e = cudaLaunchKernelEx(&cfg, count, p, C);
   } else {
-    balance_count_kernel<<<(unsigned)n_seqs, kCountThreads, 0, s>>>(p, 1);
+    count<<<(unsigned)n_seqs, kCountThreads, 0, s>>>(p, 1);
     e = cudaGetLastError();
   }
   prof_end(s);
