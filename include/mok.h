@@ -278,7 +278,7 @@ size_t mok_rms_norm_workspace_size(int64_t T, int d);
  *   -> ds in bf16 in dx[T,d] (NULL to skip) and in res_type in dresidual[T,d] (NULL to skip; at
  *      least one of the two), dweight[d] fp32 (rows summed in a fixed order).
  * ds is the gradient of x and of the residual alike.  dx may be dy, dresidual may be dres or s.
- * Sizes and alignment as in mok_rms_norm.  Two launches. */
+ * Sizes and alignment as in mok_rms_norm.  Two launches, the second begins under the first. */
 int mok_rms_norm_backward(int64_t T, int d, float eps, const void *dy, const void *s, int res_type,
                           const void *weight, int weight_type, const void *dres, void *dx,
                           void *dresidual, float *dweight, void *ws, size_t ws_bytes,
@@ -314,7 +314,8 @@ size_t mok_grad_norm_workspace_size(int n_tensors, const int64_t *numel);
 
 /* Norm of all gradients together: out[2] fp32 on the device = {norm, factor} with norm the root
  * of the sum of squares over every tensor (fp32 partial sums in a fixed order, joined in 64 bits)
- * and factor = min(1, max_norm / norm) (1 when max_norm <= 0, NaN when the norm is not finite).
+ * and factor = min(1, max_norm / norm) (1 when max_norm <= 0, NaN when the norm is not finite or
+ * its square overflows fp32).
  * grads, numel and types (mok_elem) are HOST arrays of n_tensors entries; they may be reused as
  * soon as the call returns.  Tensors are 16-byte aligned; empty ones are fine. */
 int mok_grad_norm(int n_tensors, const void *const *grads, const int64_t *numel,

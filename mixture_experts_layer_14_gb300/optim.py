@@ -21,6 +21,7 @@ _TABLE = np.dtype([(n, np.uint64) for n in ("param", "grad", "master", "exp_avg"
 assert _TABLE.itemsize == ctypes.sizeof(AdamWTensor)
 
 STATE_FORMATS = {"f32": 0, "mxfp8": 1}   # mok_state_format
+STATE_KEYS = ("master", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")
 
 
 class TensorList:
@@ -103,41 +104,40 @@ class AdamW:
             raise ValueError(f"weight_decay: {len(decay)} values for {n} tensors")
         checked = TensorList(self.params)
         self.device = checked.device
-        mx = states == "mxfp8"
-        self.state = {}
-        for key in ("master", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"):
-            given = state.get(key) if state is not None else None
-            if given is not None and len(given) != n and not (key.endswith("scale") and not mx):
-                raise ValueError(f"state[{key!r}]: {len(given)} entries for {n} tensors")
-            self.state[key] = [self._buffer(key, i, p, mx, given, state is not None)
-                               for i, p in enumerate(self.params)]
         self.table = (AdamWTensor * n)()
         self._view = np.frombuffer(self.table, dtype=_TABLE) if n else np.zeros(0, dtype=_TABLE)
-        for i, p in enumerate(self.params):
-            at = {k: (v[i].data_ptr() or None) if v[i] is not None else None for k, v in self.state.items()}
-            self.table[i] = AdamWTensor(p.data_ptr() or None, None, at["master"], at["exp_avg"], at["exp_avg_sq"],
-                                        at["exp_avg_scale"], at["exp_avg_sq_scale"], p.numel(), decay[i],
-                                        _elem(p, "param"), 0)
+        self._view["param"], self._view["param_type"] = checked.view_pointers, checked.view_types
+        self._view["numel"], self._view["weight_decay"] = checked.view_numel, decay
+        self.state = {}
+        for key in STATE_KEYS:
+            buffers = self.state[key] = self._buffers(key, checked.view_numel.tolist(), state)
+            self._view[key] = [0 if t is None else t.data_ptr() for t in buffers]
 
-    @staticmethod
-    def _buffer(key, i, p, mx, given, resume):
-        scale = key.endswith("scale")
-        if (key == "master" and p.dtype == torch.float32) or (scale and not mx):
-            return None
-        if key == "master":
-            n, dtype = p.numel(), torch.float32
-        else:
-            n = (p.numel() + 31) // 32 if scale else p.numel()
-            dtype = torch.uint8 if mx else torch.float32
-        if resume:
-            given = None if given is None else given[i]
-            if given is None or given.dtype != dtype or given.numel() != n or not given.is_contiguous() \
-                    or given.device != p.device:
-                raise ValueError(f"state[{key!r}][{i}] must be {n} contiguous {dtype} elements on {p.device}")
-            return given
-        if key == "master":
-            return p.detach().to(torch.float32).reshape(-1)
-        return torch.zeros(n, dtype=dtype, device=p.device)
+    def _buffers(self, key, sizes, state):
+        """The tensors of one kind of state, None where a weight has none: new ones, or the given
+        ones checked."""
+        mx, master, scale = self.states == "mxfp8", key == "master", key.endswith("scale")
+        if scale and not mx:
+            return [None] * len(sizes)
+        given = None if state is None else state.get(key) or [None] * len(sizes)
+        if given is not None and len(given) != len(sizes):
+            raise ValueError(f"state[{key!r}]: {len(given)} entries for {len(sizes)} tensors")
+        dtype = torch.uint8 if mx and not master else torch.float32
+        out = []
+        for i, (p, n) in enumerate(zip(self.params, sizes)):
+            n = (n + 31) // 32 if scale else n
+            if master and p.dtype == torch.float32:
+                t = None
+            elif given is not None:
+                t = given[i]
+                if t is None or t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != self.device:
+                    raise ValueError(f"state[{key!r}][{i}] must be {n} contiguous {dtype} elements on {self.device}")
+            elif master:
+                t = p.detach().to(torch.float32).reshape(-1)
+            else:
+                t = torch.zeros(n, dtype=dtype, device=self.device)
+            out.append(t)
+        return out
 
     @property
     def steps(self):
