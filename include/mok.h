@@ -303,7 +303,7 @@ size_t mok_balance_loss_workspace_size(const mok_dims *dims, int64_t n_seqs);
  * Experts masked with -inf logits get probability and gradient 0; a token all of whose logits are
  * -inf gives no loss and no gradient.  An index outside [0,E) sets MOK_ERR_DEVICE_CHECK in the
  * status word of ws and its route is not counted.  dims->T, E, k are used; n_seqs >= 1,
- * n_seqs * E < 2^31.  The gradient goes into mok_moe_backward_aux. */
+ * n_seqs * E < 2^31; logits, counts, dlogits and ws are 16-byte aligned.  The gradient goes into mok_moe_backward_aux. */
 int mok_balance_loss(const mok_dims *dims, const float *logits, const int32_t *topk_idx,
                      const int32_t *seq_offsets, int64_t n_seqs, const uint8_t *token_mask,
                      float alpha, float z_coef, const float *grad, int32_t *counts, float *loss,

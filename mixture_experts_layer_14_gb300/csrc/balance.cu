@@ -207,7 +207,7 @@ __device__ __forceinline__ float2 balance_tokens(const BalanceParams& p, int64_t
       l[2 * i + 1] = make_float2(v.z, v.w);
       top = fmaxf(top, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
     }
-    fetch(t + kRing, slot);  // this place is in registers now
+    fetch(t + kRing, slot);  // the reads of this place come before in program order
     slot = slot + 1 == kRing ? 0 : slot + 1;
     if (s != s_held && s >= 0) {
       s_held = s;
@@ -371,6 +371,8 @@ int mok_balance_loss(const mok_dims* dims, const float* logits, const int32_t* t
   if (!counts || !loss || !ws || (dims->T > 0 && (!logits || !topk_idx))) return MOK_ERR_INVALID_ARG;
   for (const void* q : {(const void*)logits, (const void*)counts, (const void*)dlogits, (const void*)ws})
     if (reinterpret_cast<uintptr_t>(q) & 15u) return MOK_ERR_UNSUPPORTED;
+  for (const void* q : {(const void*)topk_idx, (const void*)seq_offsets, (const void*)grad, (const void*)loss})
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return MOK_ERR_UNSUPPORTED;
   if (ws_bytes < balance_ws(n_seqs)) return MOK_ERR_WORKSPACE;
   set_last_launches(0);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

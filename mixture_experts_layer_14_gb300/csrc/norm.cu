@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(MT) rms_norm_kernel(const __grid_constant__ No
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(h[i].v[j], h[i].v[j], ss);
     }
-    fetch(t + p.depth * step, slot);  // this place is in registers now
+    fetch(t + p.depth * step, slot);  // this thread's reads of the place come before in program order
     slot = slot + 1 == p.depth ? 0 : slot + 1;
     ss = row_sum(ss, 0.0f, smem, turn).x;
     const float rho = 1.0f / sqrtf(ss / (float)p.d + p.eps);

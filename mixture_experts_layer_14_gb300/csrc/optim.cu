@@ -514,7 +514,7 @@ int mok_grad_norm(int n_tensors, const void* const* grads, const int64_t* numel,
       return MOK_ERR_INVALID_ARG;
     if (!is16(grads[i])) return MOK_ERR_UNSUPPORTED;
   }
-  if (!is16(ws)) return MOK_ERR_UNSUPPORTED;
+  if (!is16(ws) || (reinterpret_cast<uintptr_t>(out) & 3u)) return MOK_ERR_UNSUPPORTED;
   const size_t need = mok_grad_norm_workspace_size(n_tensors, numel);
   if (need == 0) return MOK_ERR_UNSUPPORTED;
   if (ws_bytes < need) return MOK_ERR_WORKSPACE;
@@ -544,6 +544,7 @@ int mok_adamw_step(const mok_adamw_args* args, const mok_adamw_tensor* tensors, 
                    const float* clip, mok_stream_t stream) {
   using namespace mok;
   if (!args || n_tensors < 0 || (n_tensors > 0 && !tensors)) return MOK_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(clip) & 3u) return MOK_ERR_UNSUPPORTED;
   const mok_adamw_args& a = *args;
   if (!(a.beta1 >= 0.0 && a.beta1 < 1.0) || !(a.beta2 >= 0.0 && a.beta2 < 1.0) || !(a.eps >= 1e-15) ||
       !std::isfinite(a.eps) || !std::isfinite(a.lr) || a.step < 1 ||

@@ -55,7 +55,8 @@ def _balance(D=None, logits=P, idx=P, off=NULL, S=1, mask=NULL, alpha=0.1, z=0.0
     (dict(alpha=float("nan")), INVALID), (dict(z=float("inf")), INVALID), (dict(logits=NULL), INVALID),
     (dict(idx=NULL), INVALID), (dict(counts=NULL), INVALID), (dict(loss=NULL), INVALID), (dict(ws=NULL), INVALID),
     (dict(logits=ODD), UNSUPPORTED), (dict(counts=ODD), UNSUPPORTED), (dict(dl=ODD), UNSUPPORTED),
-    (dict(ws=ODD), UNSUPPORTED), (dict(n=64), WORKSPACE)])
+    (dict(ws=ODD), UNSUPPORTED), (dict(n=64), WORKSPACE), (dict(idx=0x1002), UNSUPPORTED), (dict(loss=0x1001), UNSUPPORTED),
+    (dict(off=0x1002), UNSUPPORTED), (dict(grad=0x1002), UNSUPPORTED)])
 def test_balance_loss(kw, rc):
     assert _balance(**kw) == rc
 
@@ -71,7 +72,7 @@ def _norm_of(n=1, grads=(P,), numel=(100,), types=(0,), limit=1.0, out=P, ws=P, 
     (dict(n=-1), INVALID), (dict(grads=None), INVALID), (dict(numel=None), INVALID), (dict(types=None), INVALID),
     (dict(out=NULL), INVALID), (dict(ws=NULL), INVALID), (dict(limit=float("nan")), INVALID), (dict(grads=(None,)), INVALID),
     (dict(numel=(-1,)), INVALID), (dict(types=(2,)), INVALID), (dict(grads=(ODD,)), UNSUPPORTED), (dict(ws=ODD), UNSUPPORTED),
-    (dict(numel=(1 << 41,)), UNSUPPORTED), (dict(size=128), WORKSPACE)])
+    (dict(numel=(1 << 41,)), UNSUPPORTED), (dict(size=128), WORKSPACE), (dict(out=0x1002), UNSUPPORTED)])
 def test_grad_norm(kw, rc):
     assert _norm_of(**kw) == rc
 
