@@ -360,28 +360,32 @@ def rms_norm(x, weight, eps=1e-6, residual=None, mx=None, want_y=True):
     ``moe_forward(..., x_mx=(codes, scales))`` takes)."""
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
-    T, d = x.shape
-    dev = x.device
-    _want(x, "x", (T, d), torch.bfloat16, dev)
+    shape, dev = x.shape, x.device
+    T, d = shape
+    _want(x, "x", shape, torch.bfloat16, dev)
     _want(weight, "weight", (d,), weight.dtype, dev)
-    wt = _elem(weight, "weight")
-    if mx not in (None, "rows", "atoms"):
-        raise ValueError("mx must be None, 'rows' or 'atoms'")
-    out = {}
-    if want_y:
-        out["y"] = torch.empty_like(x)
+    y = torch.empty_like(x) if want_y else None
+    h = codes = scales = None
     rt = 0
     if residual is not None:
         rt = _elem(residual, "residual")
-        _want(residual, "residual", (T, d), residual.dtype, dev)
-        out["residual"] = torch.empty_like(residual)
+        _want(residual, "residual", shape, residual.dtype, dev)
+        h = torch.empty_like(residual)
     if mx is not None:
-        out["codes"] = torch.empty((T, d), dtype=torch.uint8, device=dev)
-        n = _scale_bytes(T, d, mx)
-        out["scales"] = torch.empty((T, d // 32) if mx == "rows" else (n,), dtype=torch.uint8, device=dev)
-    _check(lib().mok_rms_norm(T, d, eps, _ptr(x), _ptr(residual), rt, _ptr(weight), wt,
-                              _ptr(out.get("y")), _ptr(out.get("residual")), _ptr(out.get("codes")),
-                              _ptr(out.get("scales")), 1 if mx == "atoms" else 0, _stream()))
+        if mx not in ("rows", "atoms"):
+            raise ValueError("mx must be None, 'rows' or 'atoms'")
+        codes = torch.empty(shape, dtype=torch.uint8, device=dev)
+        scales = torch.empty((T, d // 32) if mx == "rows" else (_scale_bytes(T, d, mx),), dtype=torch.uint8,
+                             device=dev)
+    _check(lib().mok_rms_norm(T, d, eps, x.data_ptr(), _ptr(residual), rt, weight.data_ptr(), _elem(weight, "weight"),
+                              _ptr(y), _ptr(h), _ptr(codes), _ptr(scales), 1 if mx == "atoms" else 0, _stream()))
+    out = {}
+    if want_y:
+        out["y"] = y
+    if h is not None:
+        out["residual"] = h
+    if codes is not None:
+        out["codes"], out["scales"] = codes, scales
     return out
 
 
@@ -400,23 +404,26 @@ def rms_norm_backward(dy, s, weight, eps=1e-6, dres=None, ws=None):
     rms_norm_workspace_size(T, d) bytes (allocated per call when None)."""
     if s.dim() != 2:
         raise ValueError("s must be 2-D")
-    T, d = s.shape
-    dev = s.device
-    st, wt = _elem(s, "s"), _elem(weight, "weight")
-    _want(s, "s", (T, d), s.dtype, dev)
-    _want(dy, "dy", (T, d), torch.bfloat16, dev)
+    shape, dev = s.shape, s.device
+    T, d = shape
+    st = _elem(s, "s")
+    _want(s, "s", shape, s.dtype, dev)
+    _want(dy, "dy", shape, torch.bfloat16, dev)
     _want(weight, "weight", (d,), weight.dtype, dev)
     if dres is not None:
-        _want(dres, "dres", (T, d), s.dtype, dev)
+        _want(dres, "dres", shape, s.dtype, dev)
     if ws is None:
         ws = torch.empty(rms_norm_workspace_size(T, d), dtype=torch.uint8, device=dev)
     _want_ws(ws, dev)
-    out = {"dx": torch.empty_like(dy), "dweight": torch.empty((d,), dtype=torch.float32, device=dev)}
+    dx = torch.empty_like(dy)
+    dweight = torch.empty((d,), dtype=torch.float32, device=dev)
+    ds = torch.empty_like(s) if st else None
+    _check(lib().mok_rms_norm_backward(T, d, eps, dy.data_ptr(), s.data_ptr(), st, weight.data_ptr(),
+                                       _elem(weight, "weight"), _ptr(dres), dx.data_ptr(), _ptr(ds),
+                                       dweight.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
+    out = {"dx": dx, "dweight": dweight}
     if st:
-        out["dresidual"] = torch.empty_like(s)
-    _check(lib().mok_rms_norm_backward(T, d, eps, _ptr(dy), _ptr(s), st, _ptr(weight), wt, _ptr(dres),
-                                       _ptr(out["dx"]), _ptr(out.get("dresidual")), _ptr(out["dweight"]),
-                                       _ptr(ws), ws.numel(), _stream()))
+        out["dresidual"] = ds
     return out
 
 
@@ -448,14 +455,15 @@ def balance_loss(D, logits, topk_idx, ws, alpha, z_coef=0.0, seq_offsets=None, t
     if grad is not None:
         _want(grad, "grad", (1,), torch.float32, dev)
     _want_ws(ws, dev)
-    out = {"loss": torch.empty((2,), dtype=torch.float32, device=dev),
-           "counts": torch.empty((S, D.E), dtype=torch.int32, device=dev)}
+    loss = torch.empty((2,), dtype=torch.float32, device=dev)
+    counts = torch.empty((S, D.E), dtype=torch.int32, device=dev)
+    dlogits = torch.empty_like(logits) if want_dlogits else None
+    _check(lib().mok_balance_loss(ctypes.byref(D), logits.data_ptr(), topk_idx.data_ptr(), _ptr(seq_offsets), S,
+                                  _ptr(token_mask), alpha, z_coef, _ptr(grad), counts.data_ptr(), loss.data_ptr(),
+                                  _ptr(dlogits), ws.data_ptr(), ws.numel(), _stream()))
+    out = {"loss": loss, "counts": counts}
     if want_dlogits:
-        out["dlogits"] = torch.empty_like(logits)
-    _check(lib().mok_balance_loss(ctypes.byref(D), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), S,
-                                  _ptr(token_mask), alpha, z_coef, _ptr(grad), _ptr(out["counts"]),
-                                  _ptr(out["loss"]), _ptr(out.get("dlogits")), _ptr(ws), ws.numel(),
-                                  _stream()))
+        out["dlogits"] = dlogits
     return out
 
 

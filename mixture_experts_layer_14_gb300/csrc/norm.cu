@@ -443,34 +443,33 @@ constexpr int kSmemPerSm = 227 * 1024;             // for the blocks of an SM to
 constexpr int kSmemOwn = 2048;                     // of a block: reserved and static
 constexpr int kRingBytes = kSmemPerSm - kSmemOwn;  // most dynamic bytes of a block
 constexpr int kPlainSmem = 40 * 1024;              // dynamic bytes that need no attribute
-static NormShape norm_shape(int64_t T, int d, int row_bytes, bool warp_rows) {
+static NormShape norm_shape(int sms, int64_t T, int d, int row_bytes, bool warp_rows) {
   NormShape n;
   const int nvec = d / 8;
   n.v = nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4;
   n.threads = ((nvec + n.v - 1) / n.v + 31) / 32 * 32;
   n.rows = warp_rows && n.threads == 32 ? 8 : 1;
   n.blocks = std::max(1, std::min(1024 / (n.threads * n.rows), 8));
-  const int64_t turns = (T + (int64_t)num_sms() * n.blocks * n.rows - 1) / ((int64_t)num_sms() * n.blocks * n.rows);
-  n.depth = n.blocks > 1 || turns < 2 || 2 * row_bytes > kRingBytes ? 1 : 2;
+  n.depth = n.blocks > 1 || T <= (int64_t)sms * n.blocks * n.rows || 2 * row_bytes > kRingBytes ? 1 : 2;
   return n;
 }
 // Backward: two rows at least, three where they fit, or depth 0 where not even two do.  dres goes
 // through the ring in bf16 where three rows with it fit; in fp32 it comes straight to registers
 // (2^26 elements at d = 7168: 165 us against 198 through the ring, 158 at the copy rate).
-static NormShape norm_bwd_shape(int64_t T, int d, bool f32, bool dres, int* row_bytes, int* ring_res) {
+static NormShape norm_bwd_shape(int sms, int64_t T, int d, bool f32, bool dres, int* row_bytes, int* ring_res) {
   const int plane = 2 * d, planes = f32 ? 2 : 1;
-  NormShape n = norm_shape(T, d, plane, false);
+  NormShape n = norm_shape(sms, T, d, plane, false);
   const int room = kSmemPerSm / n.blocks - kSmemOwn;
   *ring_res = dres && !f32 && 9 * plane <= room;
   *row_bytes = plane * (1 + planes * (*ring_res ? 2 : 1));
   n.depth = std::min(3, room / *row_bytes);
-  const int64_t turns = (T + (int64_t)num_sms() * n.blocks - 1) / ((int64_t)num_sms() * n.blocks);
+  const int64_t turns = (T + (int64_t)sms * n.blocks - 1) / ((int64_t)sms * n.blocks);
   n.depth = n.depth < 2 ? 0 : (int)std::min<int64_t>(n.depth, turns + 1);
   return n;
 }
 // The same for every type, so that one workspace size serves them all.
-static int norm_bwd_grid(int64_t T, int d) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(T, (int64_t)num_sms() * norm_shape(T, d, 2 * d, false).blocks));
+static int norm_bwd_grid(int sms, int64_t T, int d) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(T, (int64_t)sms * norm_shape(sms, T, d, 2 * d, false).blocks));
 }
 static bool is16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -498,10 +497,11 @@ int mok_rms_norm(int64_t T, int d, float eps, const void* x, const void* residua
                weight_type == MOK_T_F32, scale_layout == MOK_SCALES_ATOMS, 1};
   if (codes && p.atoms) p.rows = (T + 127) / 128 * 128;
   const int row_bytes = 2 * d * (1 + (!residual ? 0 : res_type == MOK_T_F32 ? 2 : 1));
-  const NormShape n = norm_shape(T, d, row_bytes, true);
+  const int sms = num_sms();
+  const NormShape n = norm_shape(sms, T, d, row_bytes, true);
   p.depth = n.depth;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int grid = (int)std::min<int64_t>((p.rows + n.rows - 1) / n.rows, (int64_t)num_sms() * n.blocks);
+  const int grid = (int)std::min<int64_t>((p.rows + n.rows - 1) / n.rows, (int64_t)sms * n.blocks);
   void (*k)(const NormParams) = nullptr;
   auto pick = [&](auto res) {
     constexpr int R = decltype(res)::value;
@@ -525,7 +525,7 @@ int mok_rms_norm(int64_t T, int d, float eps, const void* x, const void* residua
 size_t mok_rms_norm_workspace_size(int64_t T, int d) {
   using namespace mok;
   if (!norm_sizes_ok(T, d)) return 0;
-  return 256 + sizeof(float) * (size_t)norm_bwd_grid(T, d) * d;
+  return 256 + sizeof(float) * (size_t)norm_bwd_grid(num_sms(), T, d) * d;
 }
 
 int mok_rms_norm_backward(int64_t T, int d, float eps, const void* dy, const void* s, int res_type,
@@ -540,7 +540,8 @@ int mok_rms_norm_backward(int64_t T, int d, float eps, const void* dy, const voi
   if (!dweight || !ws || (T > 0 && (!dy || !s || !weight || (!dx && !dresidual)))) return MOK_ERR_INVALID_ARG;
   for (const void* q : {dy, s, weight, dres, (const void*)dx, (const void*)dresidual, (const void*)dweight, (const void*)ws})
     if (!is16(q)) return MOK_ERR_UNSUPPORTED;
-  if (ws_bytes < mok_rms_norm_workspace_size(T, d)) return MOK_ERR_WORKSPACE;
+  const int sms = num_sms(), grid = norm_bwd_grid(sms, T, d);
+  if (ws_bytes < 256 + sizeof(float) * (size_t)grid * d) return MOK_ERR_WORKSPACE;
   set_last_launches(0);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (T == 0) return cudaMemsetAsync(dweight, 0, sizeof(float) * d, st) == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
@@ -548,9 +549,8 @@ int mok_rms_norm_backward(int64_t T, int d, float eps, const void* dy, const voi
   NormBwdParams p{dy, s, dres, weight, dx, dresidual, partial, T, d, eps, 1.0f / (float)d, weight_type == MOK_T_F32, 0, 0};
   int row_bytes;
   const bool f32 = res_type == MOK_T_F32;
-  const NormShape n = norm_bwd_shape(T, d, f32, dres != nullptr, &row_bytes, &p.ring_res);
+  const NormShape n = norm_bwd_shape(sms, T, d, f32, dres != nullptr, &row_bytes, &p.ring_res);
   p.depth = n.depth;
-  const int grid = norm_bwd_grid(T, d);
   void (*k)(const NormBwdParams) = nullptr;
   auto pick = [&](auto type, auto has) {
     constexpr bool F = decltype(type)::value, R = decltype(has)::value;

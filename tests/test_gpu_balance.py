@@ -71,7 +71,7 @@ def test_one_sequence(T, E, k, z):
 
 
 @pytest.mark.parametrize("T,E,k,S", [(50, 8, 2, 50), (400, 24, 3, 7), (1000, 256, 8, 5), (513, 384, 4, 100),
-                                     (3000, 64, 8, 700)])
+                                     (3000, 64, 8, 700), (3000, 16, 2, 2500), (6000, 24, 4, 3)])
 def test_packed_and_masked(T, E, k, S):
     """Ragged sequences, some empty, tokens before the first and after the last, masked tokens."""
     ensure_lib()
@@ -81,6 +81,22 @@ def test_packed_and_masked(T, E, k, S):
     logits, idx = _inputs(T, E, k, S)
     _check(logits, idx, 0.02, 1e-3, cuts, rng.random(T) < 0.7)
     _check(logits, idx, 0.02, 0.0, [0] + cuts[1:-1] + [T], None)
+
+
+@pytest.mark.parametrize("k", [4, 8])
+def test_selection_that_is_not_16_byte_aligned(k):
+    ensure_lib()
+    logits, idx = _inputs(900, 32, k, 12)
+    D = mok.dims(900, 128, 32, k, 128, 0, 0)
+    ws = torch.zeros(mok.balance_loss_workspace_size(D), dtype=torch.uint8, device="cuda")
+    shifted = torch.empty(900 * k + 2, dtype=torch.int32, device="cuda")[2:].view(900, k)
+    shifted.copy_(idx)
+    want, _ = _run(logits, idx, 0.02, 1e-3)
+    got = mok.balance_loss(D, logits.cuda(), shifted, ws, 0.02, z_coef=1e-3)
+    assert all(torch.equal(want[key], got[key]) for key in want)
+    with pytest.raises(mok.MokError):
+        moved = torch.empty(900 * 32 + 1, device="cuda")[1:].view(900, 32)
+        mok.balance_loss(D, moved, shifted, ws, 0.02)
 
 
 def test_everything_masked():

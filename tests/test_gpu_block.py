@@ -102,6 +102,25 @@ def test_block_forward_and_backward(dtype, res):
                                                      idx, oracle.weights_for_selection(logits, idx)))
 
 
+def test_block_without_a_shared_expert():
+    ensure_lib()
+    shape = MX.with_(dtype="bf16", n_shared=0, F_shared=0)
+    D = dims_of(shape)
+    W = to_dev(make_layer(shape, "cpu", with_dy=True))
+    x, dY = W.pop("x"), W.pop("dY")
+    W["norm"] = torch.ones(shape.d, dtype=torch.bfloat16, device="cuda")
+    b = mok.MoEBlock(D, W, alpha=0.1)
+    with pytest.raises(RuntimeError):
+        b.backward(dY)
+    b.forward(x, training=True)
+    names, params = b.parameters()
+    grads = b.gradients(b.backward(dY))
+    assert names == ["W_router", "W_gate", "W_up", "W_down", "norm"]
+    assert all(p.shape == q.shape and q.isfinite().all() for p, q in zip(params, grads))
+    mok.AdamW(params).step(grads, 1e-3, clip=mok.grad_norm(grads, 1.0))
+    assert b.forward(x)[0].isfinite().all()
+
+
 @pytest.mark.parametrize("dtype,states", [("bf16", "f32"), ("bf16", "mxfp8"), ("mxfp8", "f32"), ("mxfp8", "mxfp8")])
 def test_training_reduces_the_error(dtype, states):
     ensure_lib()
