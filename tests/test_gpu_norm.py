@@ -168,6 +168,23 @@ def test_in_place_and_side_stream():
     assert torch.equal(got["y"], want["y"])
 
 
+@pytest.mark.parametrize("T,d", [(700, 1024), (400, 7168), (330, 24576)])
+@pytest.mark.parametrize("over", ["dres", "s"])
+def test_backward_in_place(T, d, over):
+    """dx over dy, dresidual over dres or over s, with and without rows in shared memory."""
+    ensure_lib()
+    s, dy, w, dres = _cuda(_rows(T, d, torch.float32, 30), _rows(T, d, torch.bfloat16, 31), _weight(d, torch.float32, 32),
+                           _rows(T, d, torch.float32, 33))
+    want = mok.rms_norm_backward(dy, s, w, EPS, dres=dres)
+    ws = torch.zeros(mok.rms_norm_workspace_size(T, d), dtype=torch.uint8, device="cuda")
+    dweight = torch.empty(d, device="cuda")
+    target = dres if over == "dres" else s
+    assert mok.lib().mok_rms_norm_backward(T, d, EPS, dy.data_ptr(), s.data_ptr(), 1, w.data_ptr(), 1, dres.data_ptr(),
+                                           dy.data_ptr(), target.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
+                                           ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(dy, want["dx"]) and torch.equal(target, want["dresidual"]) and torch.equal(dweight, want["dweight"])
+
+
 def test_zero_rows_and_non_finite_rows():
     """A zero row gives zeros; a row with inf or NaN does not touch the others."""
     ensure_lib()
