@@ -159,11 +159,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // sequence stay in registers); the warp's {sum a <c, p>, sum lse^2}, the same in all lanes.  Lane i holds the 4-element vectors i, i + 32, ... of a
 // token's logits (EV of them); the next kRing tokens' come into a ring in shared memory by
 // asynchronous copies, each lane's to where it reads them back itself.  exp(l - max) is
-// 2^(l log2 e - m) with one rounding of the exponent; m is the same for the whole row, so that its
-// own rounding cancels in the softmax and enters lse once.
+// 2^((l - max) log2 e), the difference first: l log2 e overflows for finite logits, and from 2e9 on
+// its rounding alone is more than the exponential's range.
 // ready() comes before the first use of counts and n_seq and returns the number of valid tokens;
 // sequence(t, s) is the sequence of a token, or -1, s the one of a token before it, or -1.
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int ring_of(int ev) { return ev == 4 ? 2 : 3; }  // rows; at most 36 KB per block
 template <int EV, class Ready, class Sequence>
 __device__ __forceinline__ float2 balance_tokens(const BalanceParams& p, int64_t t, int64_t end, uint32_t ring,
@@ -224,11 +224,11 @@ __device__ __forceinline__ float2 balance_tokens(const BalanceParams& p, int64_t
     float q = 0.0f, inner = 0.0f, b = 0.0f;
     if (live) {
       top = warp_max(top);
-      const float m = top == -INFINITY ? 0.0f : top * kLog2e;
+      if (top == -INFINITY) top = 0.0f;
       float2 total2 = make_float2(0.0f, 0.0f), inner2 = total2;
 #pragma unroll
       for (int i = 0; i < 2 * EV; ++i) {
-        const float2 x = __ffma2_rn(l[i], make_float2(kLog2e, kLog2e), make_float2(-m, -m));
+        const float2 x = __fmul2_rn(__fadd2_rn(l[i], make_float2(-top, -top)), make_float2(kLog2e, kLog2e));
         l[i] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
         total2 = __fadd2_rn(total2, l[i]);
         inner2 = __ffma2_rn(c[i], l[i], inner2);
@@ -239,7 +239,7 @@ __device__ __forceinline__ float2 balance_tokens(const BalanceParams& p, int64_t
         r = __fadd2_rn(r, make_float2(__shfl_xor_sync(0xffffffffu, r.x, o), __shfl_xor_sync(0xffffffffu, r.y, o)));
       live = r.x != 0.0f;  // nothing but -inf: no loss, no gradient (a NaN total stays live)
       if (live) {
-        const float inv = 1.0f / r.x, lse = m * kLn2 + logf(r.x);
+        const float inv = 1.0f / r.x, lse = top + logf(r.x);
         inner = r.y * inv;
         b = b_all * lse;
         sum.x += a * inner;
