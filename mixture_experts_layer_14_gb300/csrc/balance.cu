@@ -27,7 +27,7 @@ struct BalanceParams {
   const float* grad;           // or NULL
   int32_t* counts;             // [S, E]
   int32_t* n_seq;              // [S], then the ticket of the pass's blocks
-  float2* partial;             // [blocks] {sum a <c, p>, sum lse^2}
+  float2* partial;             // [blocks] {sum a <c, p>, sum b lse^2}
   float* loss;
   float* dlogits;              // or NULL
   int* status;
@@ -156,7 +156,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // Losses and gradients of the tokens [t, end) of a warp (neighbours, so that the counts of their
-// sequence stay in registers); the warp's {sum a <c, p>, sum lse^2}, the same in all lanes.  Lane i holds the 4-element vectors i, i + 32, ... of a
+// sequence stay in registers); the warp's {sum a <c, p>, sum b lse^2}, the same in all lanes.  Lane i holds the 4-element vectors i, i + 32, ... of a
 // token's logits (EV of them); the next kRing tokens' come into a ring in shared memory by
 // asynchronous copies, each lane's to where it reads them back itself.  exp(l - max) is
 // 2^((l - max) log2 e), the difference first: l log2 e overflows for finite logits, and from 2e9 on
@@ -167,7 +167,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int ring_of(int ev) { return ev == 4 ? 2 : 3; }  // rows; at most 36 KB per block
 template <int EV, class Ready, class Sequence>
 __device__ __forceinline__ float2 balance_tokens(const BalanceParams& p, int64_t t, int64_t end, uint32_t ring,
-                                                 Ready ready, Sequence sequence, float* inv_n_out) {
+                                                 Ready ready, Sequence sequence) {
   constexpr int kRing = ring_of(EV);
   const int lane = threadIdx.x & 31, nvec = p.E / 4;
   ring += 16 * lane;
@@ -185,7 +185,6 @@ __device__ __forceinline__ float2 balance_tokens(const BalanceParams& p, int64_t
   for (int k = 0; k < kRing; ++k) fetch(t + k, k);
   uint32_t mask_now = mask(t), mask_next = mask(t + 1);
   const float inv_n = 1.0f / (float)max(ready(), 1);
-  *inv_n_out = inv_n;
   const float g = p.grad ? *p.grad : 1.0f;
   const float a_all = p.alpha * (float)p.E / (float)p.k * inv_n, b_all = 2.0f * p.z_coef * inv_n;
   float2 sum = make_float2(0.0f, 0.0f);
@@ -243,7 +242,7 @@ __device__ __forceinline__ float2 balance_tokens(const BalanceParams& p, int64_t
         inner = r.y * inv;
         b = b_all * lse;
         sum.x += a * inner;
-        sum.y += lse * lse;
+        sum.y += b * lse;  // not lse^2 alone: it may overflow where the z loss does not, or is off
         q = g * inv;
       }
     }
@@ -276,9 +275,9 @@ __device__ __forceinline__ float2 block_join(float2 v, float2* smem, int warps) 
   }
   return v;
 }
-__device__ __forceinline__ void write_loss(const BalanceParams& p, float2 v, float inv_n) {
+__device__ __forceinline__ void write_loss(const BalanceParams& p, float2 v) {
   p.loss[0] = v.x;
-  p.loss[1] = v.y * p.z_coef * inv_n;
+  p.loss[1] = 0.5f * v.y;  // b = 2 z_coef / n
 }
 
 // Valid tokens of all sequences (every thread of the block calls this).
@@ -308,7 +307,6 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocksPerSm) balance_grad_ker
   __shared__ int32_t own_offsets[kOffsets];
   __shared__ bool last;
   const int lane = threadIdx.x & 31;
-  float inv_n;
   extern __shared__ __align__(16) uint8_t ring[];
   const int32_t* offsets = nullptr;
   auto ready = [&]() {
@@ -323,8 +321,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocksPerSm) balance_grad_ker
                                 [&](int64_t t, int s) {
                                   if (s >= 0 && (!offsets || t < offsets[s + 1])) return s;
                                   return sequence_of(offsets, p.S, t, lane);
-                                },
-                                &inv_n);
+                                });
   v = block_join(v, smem, kWarps);
   if (threadIdx.x == 0) {
     p.partial[blockIdx.x] = v;
@@ -341,7 +338,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocksPerSm) balance_grad_ker
     v.y += u.y;
   }
   v = block_join(make_float2(warp_sum(v.x), warp_sum(v.y)), smem, kWarps);
-  if (threadIdx.x == 0) write_loss(p, v, inv_n);
+  if (threadIdx.x == 0) write_loss(p, v);
 }
 
 static size_t balance_ws(int64_t S) {

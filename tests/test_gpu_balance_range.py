@@ -1,4 +1,4 @@
-"""The balance loss over the whole range of fp32 logits.
+"""Balance and z loss over the whole range of fp32 logits.
 
 Tolerances.  u = 2^-24.  A softmax entry carries two roundings of its exponent, at most 2 u |l - max|
 <= 60 u for |l - max| <= 30, the exponential's 2 ulp, the sum over at most 512 terms (lanes, then 5
@@ -93,3 +93,18 @@ def test_one_huge_logit(z):
     loss, counts, dl, size = _plain(logits, idx, 0.02, z)
     assert abs(float(out["loss"][0]) - float(loss[0])) <= TOL * float(loss[0])
     assert ((out["dlogits"].double() - dl).abs() <= TOL * size + 1e-30).all()
+
+
+@pytest.mark.parametrize("value", HUGE)
+@pytest.mark.parametrize("z", [0.0, 1e-3])
+def test_z_loss_of_huge_logits(value, z):
+    """Zero when it is off, the value wherever fp32 holds it, though log-sum-exp squared overflows."""
+    ensure_lib()
+    logits, idx = _logits(50, 16, 2, 3)
+    logits[7] = value
+    got = float(_run(logits, idx, 0.02, z)["loss"][1])
+    want = float(_plain(logits, idx, 0.02, z)[0][1])
+    if want > torch.finfo(torch.float32).max:
+        assert got == float("inf")
+    else:
+        assert abs(got - want) <= TOL * want
