@@ -581,7 +581,8 @@ def host_extra_size(D):
 
 
 class MoELayer:
-    """Holds the weights of one layer and its workspaces; calls the C ABI in sequence."""
+    """Holds the weights of one layer and its workspaces; calls the C ABI in sequence.  ``backward``
+    belongs to the last forward with training=True, whatever ran for inference since."""
 
     def __init__(self, D, W, device=None):
         self.D = D
@@ -589,6 +590,7 @@ class MoELayer:
         dev = device or W["W_gate"].device
         self.ws = torch.zeros(workspace_size(D), dtype=torch.uint8, device=dev)
         self.saved = None
+        self._trained = None  # the routing that ``saved`` belongs to
         self._ws_bwd = None
 
     def forward(self, x, training=False, x_mx=None, want_logits=False):
@@ -599,17 +601,23 @@ class MoELayer:
         n += last_launch_count()
         if training and self.saved is None:
             self.saved = torch.empty(saved_size(self.D), dtype=torch.uint8, device=x.device)
+        if training:
+            self._trained = None
         y = moe_forward(self.D, self.W, x, routing, self.ws, saved=self.saved if training else None,
                         x_mx=x_mx)
         self.last_launches = n + last_launch_count()  # kernels this call enqueued
         self.routing = routing
+        if training:
+            self._trained = routing
         return y
 
     def backward(self, x, dY, dlogits_aux=None):
+        if self._trained is None:
+            raise MokError("backward needs a forward with training=True")
         if self._ws_bwd is None:
             self._ws_bwd = torch.zeros(workspace_size(self.D, backward=True), dtype=torch.uint8,
                                        device=x.device)
-        g = moe_backward(self.D, self.W, x, dY, self.saved, self.routing, self._ws_bwd,
+        g = moe_backward(self.D, self.W, x, dY, self.saved, self._trained, self._ws_bwd,
                          dlogits_aux=dlogits_aux)
         self.last_launches = last_launch_count()
         return g

@@ -29,6 +29,7 @@ class MoEBlock:
             self.requantise()
         self.layer = MoELayer(D, W)
         self.aux = None
+        self._trained = None  # u, h and the losses' gradient of the pass that backward belongs to
         self._ws = {}
 
     def requantise(self):
@@ -46,6 +47,8 @@ class MoEBlock:
         """(y, h): the block's output [T,d] bf16 and the new residual (x itself without one).  In
         training the balance and z losses are in ``self.aux`` (a dict, see
         :func:`balance_loss`)."""
+        if training:
+            self.aux = self._trained = None
         n = rms_norm(x, self.W["norm"], self.eps, residual=residual, mx="atoms" if self.mx else None)
         self.u, self.h = n["y"], n.get("residual", x)
         y = self.layer.forward(self.u, training=training, want_logits=training,
@@ -56,18 +59,20 @@ class MoEBlock:
                                     self._workspace("balance", balance_loss_workspace_size(self.D, S)),
                                     self.alpha, z_coef=self.z_coef, seq_offsets=seq_offsets,
                                     token_mask=token_mask)
+            self._trained = self.u, self.h, self.aux["dlogits"]
         return y, self.h
 
     def backward(self, dy, dh=None):
-        """Gradients for upstream dy of the output and dh of the new residual (or None): the
-        layer's dict plus "norm" (dweight, fp32), "dinput" (the gradient of x, bf16, and of a bf16
+        """Gradients of the last forward with training=True (whatever ran for inference since) for
+        upstream dy of the output and dh of the new residual (or None): the layer's dict plus "norm" (dweight, fp32), "dinput" (the gradient of x, bf16, and of a bf16
         residual) and, for an fp32 residual, "dresidual".  The gradient of the losses in
         ``self.aux`` is included."""
-        if self.aux is None:
+        if self._trained is None:
             raise RuntimeError("backward needs a forward with training=True")
-        g = self.layer.backward(self.u, dy, dlogits_aux=self.aux["dlogits"])
+        u, h, dlogits = self._trained
+        g = self.layer.backward(u, dy, dlogits_aux=dlogits)
         ws = self._workspace("norm", rms_norm_workspace_size(self.D.T, self.D.d))
-        n = rms_norm_backward(g["dX"], self.h, self.W["norm"], self.eps, dres=dh, ws=ws)
+        n = rms_norm_backward(g["dX"], h, self.W["norm"], self.eps, dres=dh, ws=ws)
         g["norm"] = n["dweight"]
         g["dinput"] = n["dx"]
         if "dresidual" in n:
