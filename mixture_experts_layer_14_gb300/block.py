@@ -26,7 +26,9 @@ class MoEBlock:
         self.D, self.W, self.eps, self.alpha, self.z_coef = D, W, eps, alpha, z_coef
         self.mx = D.dtype == MOK_MXFP8
         if self.mx and W.get("prepared") is None:
-            self.requantise()
+            W["prepared"] = prepare_weights(D, W)
+        if self.mx and W.get("prepared_bwd") is None:
+            W["prepared_bwd"] = prepare_weights_bwd(D, W)
         self.layer = MoELayer(D, W)
         self.aux = None
         self._trained = None  # u, h and the losses' gradient of the pass that backward belongs to

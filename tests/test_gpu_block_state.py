@@ -58,3 +58,16 @@ def test_a_training_forward_that_fails_leaves_nothing_to_backward():
         b.forward(x, training=True, token_mask=torch.ones(3, dtype=torch.bool, device="cuda"))
     with pytest.raises(RuntimeError):
         b.backward(dY)
+
+
+@pytest.mark.parametrize("missing", ["prepared", "prepared_bwd"])
+def test_either_prepared_form_is_made_when_it_is_missing(missing):
+    ensure_lib()
+    D, W, x, dY, b = _block("mxfp8")
+    b.forward(x, training=True)
+    want = b.backward(dY)
+    del W[missing]
+    c = mok.MoEBlock(D, W, alpha=0.1, z_coef=1e-2)
+    c.forward(x, training=True)
+    got = c.backward(dY)
+    assert torch.equal(want["dinput"], got["dinput"]) and torch.equal(want["dW_down"], got["dW_down"])
