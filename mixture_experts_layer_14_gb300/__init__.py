@@ -258,6 +258,10 @@ def _weights_struct(D, W):
         _want(W["Ws_gate"], "Ws_gate", (D.d, D.F_shared), bf, dev)
         _want(W["Ws_up"], "Ws_up", (D.d, D.F_shared), bf, dev)
         _want(W["Ws_down"], "Ws_down", (D.F_shared, D.d), bf, dev)
+    if D.dtype != MOK_BF16 and W.get("prepared") is not None:
+        _want(W["prepared"], "prepared", (prepared_size(D),), torch.uint8, dev)
+    if D.dtype == MOK_MXFP8 and W.get("prepared_bwd") is not None:
+        _want(W["prepared_bwd"], "prepared_bwd", (lib().mok_prepared_bwd_size(ctypes.byref(D)),), torch.uint8, dev)
     return Weights(
         W["W_router"].data_ptr(), W["bias"].data_ptr() if W.get("bias") is not None else None,
         W["W_gate"].data_ptr(), W["W_up"].data_ptr(), W["W_down"].data_ptr(),

@@ -71,3 +71,20 @@ def test_either_prepared_form_is_made_when_it_is_missing(missing):
     c.forward(x, training=True)
     got = c.backward(dY)
     assert torch.equal(want["dinput"], got["dinput"]) and torch.equal(want["dW_down"], got["dW_down"])
+
+
+def test_weights_prepared_for_another_dtype_are_refused():
+    """The NVFP4 form is smaller than the MXFP8 one: it must not reach an MXFP8 kernel."""
+    ensure_lib()
+    D, W, x, dY, b = _block("mxfp8")
+    nv = mok.dims(D.T, D.d, D.E, D.k, D.F, D.F_shared, 1, mok.MOK_NVFP4)
+    right = dict(W)
+    W["prepared"] = mok.prepare_weights(nv, W)
+    assert W["prepared"].numel() < right["prepared"].numel()
+    with pytest.raises(ValueError):
+        b.forward(x, training=True)
+    W["prepared"], W["prepared_bwd"] = right["prepared"], right["prepared_bwd"][:-1]
+    with pytest.raises(ValueError):
+        b.forward(x, training=True)
+    with pytest.raises(ValueError):
+        mok.moe_forward(nv, right, x, None, b.layer.ws)
