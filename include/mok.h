@@ -331,7 +331,8 @@ int mok_grad_norm(int n_tensors, const void *const *grads, const int64_t *numel,
  * that move by less than half a code per step still move.  exp_avg_sq > 0 never takes code 0. */
 typedef enum { MOK_STATE_F32 = 0, MOK_STATE_MXFP8 = 1 } mok_state_format;
 
-/* One tensor of mok_adamw_step (device pointers, 16-byte aligned; the scales need not be). */
+/* One tensor of mok_adamw_step (device pointers, 16-byte aligned; the scales need not be).  No two
+ * buffers of a call share memory, except that gradients may. */
 typedef struct {
   void *param;               /* [numel] of param_type, updated */
   const void *grad;          /* [numel] of grad_type */

@@ -84,7 +84,7 @@ class AdamW:
     """AdamW over a list of weights, one launch per step (up to 384 tensors; more take several).
 
     ``params``: bf16 or fp32 CUDA tensors, updated in place (held, with their addresses: they must
-    not be given other storage).  The learning rate and the step's number are constants of the
+    not be given other storage), no two of them on the same memory.  The learning rate and the step's number are constants of the
     launch, in a captured CUDA graph too.  A bf16 weight has an fp32 master that
     the steps accumulate in.  ``states``: "f32", or "mxfp8" for E4M3 codes with one power-of-two
     scale per 32 elements and dithered rounding (1.03 bytes per state and element; mok.h,
@@ -112,6 +112,17 @@ class AdamW:
         for key in STATE_KEYS:
             buffers = self.state[key] = self._buffers(key, checked.view_numel.tolist(), state)
             self._view[key] = [0 if t is None else t.data_ptr() for t in buffers]
+        self._check_disjoint()
+
+    def _check_disjoint(self):
+        """One launch updates everything, so no element may be reached twice (tied weights are one
+        entry, with the sum of their gradients)."""
+        tensors = [t for t in [*self.params, *sum(self.state.values(), [])] if t is not None and t.numel()]
+        start = np.array([t.data_ptr() for t in tensors], dtype=np.uint64)
+        end = start + np.array([t.numel() * t.element_size() for t in tensors], dtype=np.uint64)
+        order = np.argsort(start)
+        if (start[order][1:] < end[order][:-1]).any():
+            raise ValueError("weights and states must not share memory")
 
     def _buffers(self, key, sizes, state):
         """The tensors of one kind of state, None where a weight has none: new ones, or the given
