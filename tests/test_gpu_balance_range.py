@@ -1,4 +1,4 @@
-"""Balance and z loss over the whole range of fp32 logits.
+"""Balance and z loss over the whole range of fp32 logits, and where a warp takes many tokens.
 
 Tolerances.  u = 2^-24.  A softmax entry carries two roundings of its exponent, at most 2 u |l - max|
 <= 60 u for |l - max| <= 30, the exponential's 2 ulp, the sum over at most 512 terms (lanes, then 5
@@ -7,6 +7,7 @@ relative to p (a (c + <c,p>) + b |lse|), with 256 u.  The losses are sums of ter
 warp adds at most T / 2000 + 1 of them, then 8 warps, 4 per thread and 5 + 8 more: 256 u too.
 """
 
+import numpy as np
 import pytest
 import torch
 
@@ -108,3 +109,24 @@ def test_z_loss_of_huge_logits(value, z):
         assert got == float("inf")
     else:
         assert abs(got - want) <= TOL * want
+
+
+@pytest.mark.parametrize("T,E,k", [(40001, 128, 8), (30011, 256, 4), (20011, 384, 8), (33333, 512, 5)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_many_tokens_per_warp(T, E, k, packed):
+    """Warps take 6 to 11 tokens each, so that every place of their ring is filled again, and
+    sequences end within a warp's tokens; every row is compared."""
+    ensure_lib()
+    logits, idx = _logits(T, E, k, T)
+    offsets = mask = None
+    if packed:
+        rng = np.random.default_rng(T)
+        cuts = np.sort(rng.integers(3, T - 3, 301)).astype(np.int32)
+        offsets = torch.from_numpy(cuts).cuda()
+        mask = torch.from_numpy(rng.random(T) < 0.8).cuda()
+    z = 1e-3 if packed else 0.0
+    out = _run(logits, idx, 0.02, z, offsets, mask)
+    loss, counts, dl, size = _plain(logits, idx, 0.02, z, offsets, mask)
+    assert torch.equal(out["counts"].double(), counts)
+    assert ((out["loss"].double() - loss).abs() <= TOL * loss.abs()).all()
+    assert ((out["dlogits"].double() - dl).abs() <= TOL * size + 1e-30).all()
