@@ -1,11 +1,14 @@
-"""What a block and a layer keep between their forward and backward passes."""
+"""What a block and a layer keep between their forward and backward passes, and the layer on codes
+that it is given."""
 
+import numpy as np
 import pytest
 import torch
 
 import mixture_experts_layer_14_gb300 as mok
+import oracle
 from mixture_experts_layer_14_gb300.synthetic import LayerShape, make_layer
-from tests._helpers import dims_of, ensure_lib, to_dev
+from tests._helpers import assert_close, dims_of, ensure_lib, f64, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +91,43 @@ def test_weights_prepared_for_another_dtype_are_refused():
         b.forward(x, training=True)
     with pytest.raises(ValueError):
         mok.moe_forward(nv, right, x, None, b.layer.ws)
+
+
+def test_forward_from_given_codes_on_a_workspace_of_its_own():
+    """A zeroed workspace holds no codes of x: the output comes from the given ones."""
+    ensure_lib()
+    D = dims_of(MX, dtype=mok.MOK_MXFP8)
+    L = to_dev(make_layer(MX, "cpu"))
+    L["prepared"] = mok.prepare_weights(D, L)
+    ws = torch.zeros(mok.workspace_size(D), dtype=torch.uint8, device="cuda")
+    idx, w, _ = mok.route(D, L["x"], L["W_router"], L["bias"], ws)
+    routing = mok.dispatch_index(D, idx, w, ws)
+    want = mok.moe_forward(D, L, L["x"], routing, ws)
+    q, sc = mok.mx_quantize_rows(L["x"])
+    rows = torch.zeros((256, MX.d // 32), dtype=torch.uint8, device="cuda")
+    rows[:MX.T] = sc
+    atoms = rows.view(2, 4, 32, MX.d // 128, 4).permute(0, 3, 2, 1, 4).contiguous().view(-1)
+    fresh = torch.zeros_like(ws)
+    got = mok.moe_forward(D, L, torch.zeros_like(L["x"]), routing, fresh, x_mx=(q, atoms))
+    assert torch.equal(got, want) and mok.read_status(fresh) == 0
+
+
+def _oracle_forward(dtype, u, W, idx, weights):
+    run = oracle.moe_forward_mxfp8 if dtype == "mxfp8" else oracle.moe_forward
+    sh = (f64(W["Ws_gate"]), f64(W["Ws_up"]), f64(W["Ws_down"]))
+    return run(u, f64(W["W_gate"]), f64(W["W_up"]), f64(W["W_down"]), sh, idx, weights)
+
+
+@pytest.mark.parametrize("res", [None, torch.bfloat16, torch.float32])
+def test_mxfp8_block_output(res):
+    """The norm's codes through the layer, against the oracle on the norm in 64 bits: the quantiser
+    makes the same codes of it, but for values on a rounding boundary."""
+    ensure_lib()
+    D, W, x, dY, b = _block("mxfp8")
+    r = None if res is None else (3 * torch.randn(x.shape, generator=torch.Generator().manual_seed(2))).to(res).cuda()
+    y, _ = b.forward(x, r)
+    h = f64(x) if r is None else f64(x) + f64(r)
+    u = h / np.sqrt((h * h).mean(1, keepdims=True) + b.eps) * f64(W["norm"])
+    idx = b.layer.routing["topk_idx"].cpu().numpy()
+    logits = oracle.router_logits(f64(b.u), f64(W["W_router"]), f64(W["bias"]))
+    assert_close("y", f64(y), _oracle_forward("mxfp8", u, W, idx, oracle.weights_for_selection(logits, idx)))
