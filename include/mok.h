@@ -328,7 +328,12 @@ int mok_grad_norm(int n_tensors, const void *const *grads, const int64_t *numel,
  * (r + 1/2) / 2^16 reaches 1.  With x = 0x85EBCA6B i + 0x9E3779B9 step, x ^= x >> 15,
  * x *= 0x2C1B3C6D, x ^= x >> 12, x *= 0x297A2D39, x ^= x >> 15 (all mod 2^32), r is x's high half
  * for exp_avg and its low half for exp_avg_sq.  The mean over steps is the value, so averages
- * that move by less than half a code per step still move.  exp_avg_sq > 0 never takes code 0. */
+ * that move by less than half a code per step still move.  exp_avg_sq > 0 never takes code 0 (its
+ * step would be exp_avg / eps), so it has a lower limit, 2^-9 of the block's scale: where an
+ * element's gradients are below 1/479 to 1/339 of the largest of its 32 (which of them depends on
+ * where that one lies between two scales), exp_avg_sq is held at the limit and the step is too small
+ * by the ratio of the roots: at 1/1000 it is 0.34 to 0.48 of the exact one, at 1/3000 0.11 to 0.16.
+ * Weights whose blocks span such ratios want MOK_STATE_F32. */
 typedef enum { MOK_STATE_F32 = 0, MOK_STATE_MXFP8 = 1 } mok_state_format;
 
 /* One tensor of mok_adamw_step (device pointers, 16-byte aligned; the scales need not be).  No two

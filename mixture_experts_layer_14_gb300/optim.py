@@ -88,7 +88,9 @@ class AdamW:
     launch, in a captured CUDA graph too.  A bf16 weight has an fp32 master that
     the steps accumulate in.  ``states``: "f32", or "mxfp8" for E4M3 codes with one power-of-two
     scale per 32 elements and dithered rounding (1.03 bytes per state and element; mok.h,
-    mok_state_format).  ``weight_decay``: one value, or one per tensor.  ``state``: buffers to use
+    mok_state_format: elements whose gradients are some 400 times smaller than the largest of their 32
+    neighbours take smaller steps than they should, so that weights like W_router [d, E] under a
+    very uneven load belong to an optimiser with "f32").  ``weight_decay``: one value, or one per tensor.  ``state``: buffers to use
     (and resume from) instead of new ones, a dict of lists like :meth:`state_dict` returns."""
 
     def __init__(self, params, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, states="f32", state=None,
