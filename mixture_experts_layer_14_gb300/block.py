@@ -9,7 +9,7 @@ applies AdamW.
 
 import torch
 
-from . import (MOK_MXFP8, MoELayer, balance_loss, balance_loss_workspace_size, dims, prepare_weights,
+from . import (MOK_MXFP8, MoELayer, balance_loss, balance_loss_workspace_size, prepare_weights,
                prepare_weights_bwd, rms_norm, rms_norm_backward, rms_norm_workspace_size)
 
 __all__ = ["MoEBlock"]
@@ -82,7 +82,9 @@ class MoEBlock:
         return g
 
     def parameters(self):
-        """Names and weights, in the order of :meth:`gradients`."""
+        """Names and weights, in the order of :meth:`gradients`.  The router's "bias" is not among them:
+        it enters the logits, but the layer has no gradient for it (a program that has one moves it
+        by the counts in ``self.aux``)."""
         names = [k for k in EXPERT_WEIGHTS if self.W.get(k) is not None] + ["norm"]
         return names, [self.W[k] for k in names]
 
