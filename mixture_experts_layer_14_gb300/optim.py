@@ -119,11 +119,17 @@ class AdamW:
     def _check_disjoint(self):
         """One launch updates everything, so no element may be reached twice (tied weights are one
         entry, with the sum of their gradients)."""
-        tensors = [t for t in [*self.params, *sum(self.state.values(), [])] if t is not None and t.numel()]
-        start = np.array([t.data_ptr() for t in tensors], dtype=np.uint64)
-        end = start + np.array([t.numel() * t.element_size() for t in tensors], dtype=np.uint64)
+        v = self._view
+        n = v["numel"]
+        state = n if self.states == "mxfp8" else 4 * n
+        scale = (n + 31) // 32
+        size = np.concatenate([n * np.where(v["param_type"] == 0, 2, 4), 4 * n, state, state, scale, scale])
+        start = np.concatenate([v[key] for key in ("param", *STATE_KEYS)])
+        there = (start != 0) & (size != 0)
+        start, size = start[there], size[there].astype(np.uint64)
         order = np.argsort(start)
-        if (start[order][1:] < end[order][:-1]).any():
+        start, end = start[order], (start + size)[order]
+        if (start[1:] < end[:-1]).any():
             raise ValueError("weights and states must not share memory")
 
     def _buffers(self, key, sizes, state):
