@@ -388,6 +388,72 @@ int mok_moe_backward_aux(const mok_dims *dims, const mok_weights *w, const void 
                          float *dlogits, void *dW_router, void *ws, size_t ws_bytes,
                          mok_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Other routers, norms on both sides of a block and activations kept in 8 bits.  Same conventions.
+ * ------------------------------------------------------------------------------------------- */
+
+typedef enum { MOK_SCORE_SOFTMAX = 0, MOK_SCORE_SIGMOID = 1 } mok_score;
+typedef enum { MOK_GROUP_MAX = 0, MOK_GROUP_TOP2 = 1 } mok_group_score;
+
+/* How a router chooses experts from its logits (mok_select_experts). */
+typedef struct {
+  int32_t score;       /* mok_score */
+  int32_t n_groups;    /* groups of E / n_groups neighbouring experts; 1: none */
+  int32_t topk_groups; /* groups that stay */
+  int32_t group_score; /* mok_group_score: a group's largest key, or the sum of its two largest */
+  int32_t renormalise; /* weights over the chosen scores' sum */
+  float scale;         /* factor of the weights */
+} mok_selection;
+
+/* Choice of the experts from logits[T,E] fp32 (of mok_route): with s = softmax(logits) or
+ * sigmoid(logits) of a token and keys c = s + sel_bias (sel_bias[E] fp32 or NULL: it ranks, the
+ * weights do not see it),
+ *  - a group's score is its largest key or the sum of its two largest (its one, where it has one);
+ *    the topk_groups best groups stay;
+ *  - topk_idx[T,k] are the k largest keys of the groups that stay, in descending order (without
+ *    sel_bias the order is that of the logits);
+ *  - topk_w[T,k] = scale s_j / sum_i s_i over the chosen (0 when the sum is), or scale s_j.
+ * Ties go to the lower index.  The choice is that of exact arithmetic on the fp32 inputs: where fp32
+ * cannot tell two keys apart they are computed in 64 bits.  Experts whose logit is at or below -1e30
+ * (-inf, a type's lowest value) are shut off: s = 0, no key, chosen (lower index first) only where
+ * the groups that stay have fewer than k others; a token without open experts gets weights 0.  A
+ * bias at or below -1e30 makes its expert the last choice likewise, with its score.  A logit that is
+ * NaN, and a bias that is NaN or at or above 1e30, count as -inf and set MOK_ERR_DEVICE_CHECK in the
+ * status word of ws (256 bytes at least: any workspace of the library, zeroed once).
+ * dims->T, E, k are used; 1 <= n_groups <= 32, E % n_groups == 0, 1 <= topk_groups <= n_groups,
+ * k <= topk_groups E / n_groups, scale finite; logits, sel_bias and ws are 16-byte aligned.  One
+ * launch.  The results go into mok_dispatch_index. */
+int mok_select_experts(const mok_dims *dims, const mok_selection *sel, const float *logits,
+                       const float *sel_bias, int32_t *topk_idx, float *topk_w, void *ws,
+                       size_t ws_bytes, mok_stream_t stream);
+
+/* Gradient of the logits for dtopk_w[T,k], the gradient of mok_select_experts' weights, with the
+ * choice held constant; dlogits_aux[T,E] (of mok_balance_loss, or NULL) is added.  With p_j =
+ * s_j / sum_i s_i:
+ *   renormalised: dlogits_{e_j} = scale p_j (dw_j - sum_i p_i dw_i), times 1 - s_j for sigmoid
+ *   scores; sigmoid: scale s_j (1 - s_j) dw_j; softmax: scale s_e (dw_e - sum_i s_i dw_i) for every
+ *   expert (dw_e = 0 where e was not chosen); 0 elsewhere.
+ * An index outside [0,E) sets MOK_ERR_DEVICE_CHECK in the status word of ws and is left out; routes
+ * that name one expert twice add up.  Experts that are shut off get 0.  sel's groups are not used
+ * but checked.  logits, dlogits_aux, dlogits and ws are 16-byte aligned; dlogits may be
+ * dlogits_aux.  One launch. */
+int mok_select_experts_backward(const mok_dims *dims, const mok_selection *sel, const float *logits,
+                                const int32_t *topk_idx, const float *dtopk_w,
+                                const float *dlogits_aux, float *dlogits, void *ws, size_t ws_bytes,
+                                mok_stream_t stream);
+
+/* mok_moe_backward_aux for a routing of mok_select_experts with this sel and logits (sel NULL:
+ * exactly mok_moe_backward_aux, logits unused). */
+int mok_moe_backward_select(const mok_dims *dims, const mok_weights *w, const void *x,
+                            const void *dY, const void *saved, const mok_selection *sel,
+                            const float *logits, const int32_t *topk_idx, const float *topk_w,
+                            const int32_t *offsets, const int32_t *sorted_tok,
+                            const float *sorted_w, const int32_t *inv_pos,
+                            const float *dlogits_aux, void *dX, void *dW_gate, void *dW_up,
+                            void *dW_down, void *dWs_gate, void *dWs_up, void *dWs_down,
+                            float *dlogits, void *dW_router, void *ws, size_t ws_bytes,
+                            mok_stream_t stream);
+
 /* Schedule of the bf16 expert GEMMs of mok_moe_forward (process-wide; default
  * MOK_SCHEDULE_TWO_LAUNCHES):
  *  - MOK_SCHEDULE_TWO_LAUNCHES: gate/up + SwiGLU, then down + router weight, each one persistent

@@ -24,7 +24,7 @@ __all__ = [
     "mx_quantize_rows", "nvfp4_set_activation_amax",
     "rms_norm", "rms_norm_backward", "rms_norm_workspace_size", "balance_loss",
     "balance_loss_workspace_size", "TensorList", "grad_norm", "grad_norm_workspace_size", "AdamW",
-    "MoEBlock",
+    "MoEBlock", "Selection", "select_experts", "select_experts_backward",
 ]
 
 MOK_BF16, MOK_MXFP8, MOK_NVFP4 = 0, 1, 2
@@ -41,6 +41,7 @@ EXPORTED_SYMBOLS = [
     "mok_rms_norm", "mok_rms_norm_workspace_size", "mok_rms_norm_backward",
     "mok_balance_loss_workspace_size", "mok_balance_loss", "mok_grad_norm_workspace_size",
     "mok_grad_norm", "mok_adamw_step", "mok_moe_forward_mx", "mok_moe_backward_aux",
+    "mok_select_experts", "mok_select_experts_backward", "mok_moe_backward_select",
 ]
 
 
@@ -72,12 +73,31 @@ class AdamWArgs(ctypes.Structure):
                 ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("state_format", ctypes.c_int32)]
 
 
+class Selection(ctypes.Structure):
+    """How a router chooses experts from its logits: ``scoring`` "softmax" or "sigmoid"; ``n_groups``
+    groups of neighbouring experts, of which the ``topk_groups`` with the best ``group_score`` ("max":
+    their largest key, "top2": the sum of their two largest) stay; weights over the chosen scores'
+    sum (``renormalise``), times ``scale``.  Formulas in mok.h, mok_select_experts."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_groups", "topk_groups", "group_score", "renorm")] + [
+        ("scale", ctypes.c_float)]
+    SCORES = {"softmax": 0, "sigmoid": 1}
+    GROUP_SCORES = {"max": 0, "top2": 1}
+
+    def __init__(self, scoring="softmax", n_groups=1, topk_groups=1, group_score="max", renormalise=True, scale=1.0):
+        if scoring not in self.SCORES or group_score not in self.GROUP_SCORES:
+            raise ValueError("scoring must be 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
+        super().__init__(self.SCORES[scoring], n_groups, topk_groups, self.GROUP_SCORES[group_score],
+                         bool(renormalise), scale)
+
+
 _LIB = None
 _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I64, _INT, _F = ctypes.c_int64, ctypes.c_int, ctypes.c_float
 _DP = ctypes.POINTER(Dims)
 _WP = ctypes.POINTER(Weights)
+_SP = ctypes.POINTER(Selection)
 
 
 def lib_path():
@@ -125,6 +145,9 @@ def lib():
             "mok_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamWArgs), ctypes.POINTER(AdamWTensor), _INT, _VP, _VP]),
             "mok_moe_forward_mx": (ctypes.c_int, [_DP, _WP] + [_VP] * 10 + [_SZ, _VP]),
             "mok_moe_backward_aux": (ctypes.c_int, [_DP, _WP] + [_VP] * 20 + [_SZ, _VP]),
+            "mok_select_experts": (ctypes.c_int, [_DP, _SP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+            "mok_select_experts_backward": (ctypes.c_int, [_DP, _SP] + [_VP] * 6 + [_SZ, _VP]),
+            "mok_moe_backward_select": (ctypes.c_int, [_DP, _WP] + [_VP] * 3 + [_SP] + [_VP] * 18 + [_SZ, _VP]),
             "mok_timing_collect": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_int),
                                                   ctypes.POINTER(ctypes.c_double), ctypes.c_int,
                                                   ctypes.POINTER(ctypes.c_int)]),
@@ -471,6 +494,42 @@ def balance_loss(D, logits, topk_idx, ws, alpha, z_coef=0.0, seq_offsets=None, t
     return out
 
 
+def select_experts(D, sel, logits, ws, bias=None):
+    """Experts and weights of every token from logits [T,E] fp32 (of :func:`route`) by the rule
+    ``sel`` (a :class:`Selection`): (topk_idx [T,k] int32, topk_w [T,k] fp32), for
+    :func:`dispatch_index`.  ``bias`` fp32 [E] is added to the scores for the ranking alone; experts
+    at or below -1e30 in logits or bias are shut off.  ``ws``: any zeroed workspace of at least 256
+    bytes, whose status word reports NaN."""
+    dev = logits.device
+    _want(logits, "logits", (D.T, D.E), torch.float32, dev)
+    if bias is not None:
+        _want(bias, "bias", (D.E,), torch.float32, dev)
+    _want_ws(ws, dev)
+    idx = torch.empty((D.T, D.k), dtype=torch.int32, device=dev)
+    w = torch.empty((D.T, D.k), dtype=torch.float32, device=dev)
+    _check(lib().mok_select_experts(ctypes.byref(D), ctypes.byref(sel), logits.data_ptr(), _ptr(bias), idx.data_ptr(),
+                                    w.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
+    return idx, w
+
+
+def select_experts_backward(D, sel, logits, topk_idx, dtopk_w, ws, dlogits_aux=None):
+    """Gradient of the logits [T,E] fp32 for dtopk_w [T,k] fp32, the gradient of the weights of
+    :func:`select_experts` (the choice held constant), plus ``dlogits_aux`` [T,E] (of
+    :func:`balance_loss`).  ``ws`` as in :func:`select_experts`; reports an index outside [0,E)."""
+    dev = logits.device
+    _want(logits, "logits", (D.T, D.E), torch.float32, dev)
+    _want(topk_idx, "topk_idx", (D.T, D.k), torch.int32, dev)
+    _want(dtopk_w, "dtopk_w", (D.T, D.k), torch.float32, dev)
+    if dlogits_aux is not None:
+        _want(dlogits_aux, "dlogits_aux", (D.T, D.E), torch.float32, dev)
+    _want_ws(ws, dev)
+    dlogits = torch.empty_like(logits)
+    _check(lib().mok_select_experts_backward(
+        ctypes.byref(D), ctypes.byref(sel), logits.data_ptr(), topk_idx.data_ptr(), dtopk_w.data_ptr(),
+        _ptr(dlogits_aux), dlogits.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
+    return dlogits
+
+
 def prepared_size(D):
     return lib().mok_prepared_size(ctypes.byref(D))
 
@@ -539,12 +598,16 @@ def moe_forward(D, W, x, routing, ws, saved=None, y=None, x_mx=None):
     return y
 
 
-def moe_backward(D, W, x, dY, saved, routing, ws, want_dW_router=True, dlogits_aux=None):
+def moe_backward(D, W, x, dY, saved, routing, ws, want_dW_router=True, dlogits_aux=None, selection=None,
+                 logits=None):
     """Gradients of the layer for upstream dY (selection held constant).  Returns a dict.
     ``dlogits_aux`` [T,E] fp32: a further gradient of the logits (from :func:`balance_loss`),
-    included in dX, dW_router and dlogits."""
+    included in dX, dW_router and dlogits.  ``selection`` (with ``logits`` [T,E] fp32): the routing
+    is of :func:`select_experts`; None: of :func:`route`."""
     dev = x.device
     bf = torch.bfloat16
+    if selection is not None:
+        _want(logits, "logits", (D.T, D.E), torch.float32, dev)
     _want(dY, "dY", (D.T, D.d), bf, dev)
     if dlogits_aux is not None:
         _want(dlogits_aux, "dlogits_aux", (D.T, D.E), torch.float32, dev)
@@ -561,9 +624,10 @@ def moe_backward(D, W, x, dY, saved, routing, ws, want_dW_router=True, dlogits_a
         "dW_router": torch.empty((D.d, D.E), dtype=bf, device=dev) if want_dW_router else None,
     }
     r = routing
-    _check(lib().mok_moe_backward_aux(
-        ctypes.byref(D), ctypes.byref(ws_struct), _ptr(x), _ptr(dY), _ptr(saved), _ptr(r["topk_idx"]),
-        _ptr(r["topk_w"]), _ptr(r["offsets"]), _ptr(r["sorted_tok"]), _ptr(r["sorted_w"]),
+    _check(lib().mok_moe_backward_select(
+        ctypes.byref(D), ctypes.byref(ws_struct), _ptr(x), _ptr(dY), _ptr(saved),
+        None if selection is None else ctypes.byref(selection), None if selection is None else _ptr(logits),
+        _ptr(r["topk_idx"]), _ptr(r["topk_w"]), _ptr(r["offsets"]), _ptr(r["sorted_tok"]), _ptr(r["sorted_w"]),
         _ptr(r["inv_pos"]), _ptr(dlogits_aux), _ptr(g["dX"]), _ptr(g["dW_gate"]), _ptr(g["dW_up"]), _ptr(g["dW_down"]),
         _ptr(g["dWs_gate"]), _ptr(g["dWs_up"]), _ptr(g["dWs_down"]), _ptr(g["dlogits"]),
         _ptr(g["dW_router"]), _ptr(ws), ws.numel(), _stream()))
@@ -586,11 +650,14 @@ def host_extra_size(D):
 
 class MoELayer:
     """Holds the weights of one layer and its workspaces; calls the C ABI in sequence.  ``backward``
-    belongs to the last forward with training=True, whatever ran for inference since."""
+    belongs to the last forward with training=True, whatever ran for inference since.  ``selection``
+    (a :class:`Selection`): how experts are chosen from the router's logits, with the balance bias
+    W["balance_bias"] [E] fp32, if there is one; None: the softmax router of :func:`route`."""
 
-    def __init__(self, D, W, device=None):
+    def __init__(self, D, W, device=None, selection=None):
         self.D = D
         self.W = W
+        self.selection = selection
         dev = device or W["W_gate"].device
         self.ws = torch.zeros(workspace_size(D), dtype=torch.uint8, device=dev)
         self.saved = None
@@ -599,8 +666,11 @@ class MoELayer:
 
     def forward(self, x, training=False, x_mx=None, want_logits=False):
         idx, w, self.logits = route(self.D, x, self.W["W_router"], self.W.get("bias"), self.ws,
-                                    want_logits)
+                                    want_logits or self.selection is not None)
         n = last_launch_count()
+        if self.selection is not None:
+            idx, w = select_experts(self.D, self.selection, self.logits, self.ws, bias=self.W.get("balance_bias"))
+            n += last_launch_count()
         routing = dispatch_index(self.D, idx, w, self.ws)
         n += last_launch_count()
         if training and self.saved is None:
@@ -612,7 +682,7 @@ class MoELayer:
         self.last_launches = n + last_launch_count()  # kernels this call enqueued
         self.routing = routing
         if training:
-            self._trained = routing
+            self._trained = routing, None if self.selection is None else self.logits
         return y
 
     def backward(self, x, dY, dlogits_aux=None):
@@ -621,8 +691,9 @@ class MoELayer:
         if self._ws_bwd is None:
             self._ws_bwd = torch.zeros(workspace_size(self.D, backward=True), dtype=torch.uint8,
                                        device=x.device)
-        g = moe_backward(self.D, self.W, x, dY, self.saved, self._trained, self._ws_bwd,
-                         dlogits_aux=dlogits_aux)
+        routing, logits = self._trained
+        g = moe_backward(self.D, self.W, x, dY, self.saved, routing, self._ws_bwd, dlogits_aux=dlogits_aux,
+                         selection=self.selection, logits=logits)
         self.last_launches = last_launch_count()
         return g
 

@@ -301,7 +301,7 @@ static int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOK_OK : MOK_E
 // W_gate, W_up along F; the weight gradients' operands along each expert's tokens); the router
 // terms dl W_router^T and x^T dl stay on the bf16 path.
 static int backward_mxfp8(const mok_dims* dims, const mok_weights* w, const void* x, const void* dY,
-                          const void* saved, const int32_t* topk_idx, const float* topk_w,
+                          const void* saved, const mok_selection* sel, const float* logits, const int32_t* topk_idx, const float* topk_w,
                           const int32_t* offsets, const int32_t* sorted_tok, const float* sorted_w,
                           const int32_t* inv_pos, const float* dlogits_aux, void* dX, void* dW_gate,
                           void* dW_up, void* dW_down, void* dWs_gate, void* dWs_up, void* dWs_down,
@@ -382,8 +382,10 @@ static int backward_mxfp8(const mok_dims* dims, const mok_weights* w, const void
     ++*launches;
   }
   // 3. router backward: dw (128-column partials of <a, h>), dlogits, bf16 dl
-  rc = cuda_status(launch_router_backward(T, E, k, F / 128, topk_idx, topk_w, inv_pos, part,
-                                          dlogits_aux, dlogits, W(BW_DL), s));
+  rc = cuda_status(sel ? launch_select_backward(dims, sel, logits, topk_idx, nullptr, part, inv_pos, F / 128,
+                                                dlogits_aux, dlogits, W(BW_DL), static_cast<int*>(ws), s)
+                       : launch_router_backward(T, E, k, F / 128, topk_idx, topk_w, inv_pos, part,
+                                                dlogits_aux, dlogits, W(BW_DL), s));
   if (rc != MOK_OK) return rc;
   ++*launches;
   // 4. dX_s = dG W_gate^T + dU W_up^T
@@ -1178,8 +1180,23 @@ int mok_moe_backward_aux(const mok_dims* dims, const mok_weights* w, const void*
                          void* dW_up, void* dW_down, void* dWs_gate, void* dWs_up, void* dWs_down,
                          float* dlogits, void* dW_router, void* ws, size_t ws_bytes,
                          mok_stream_t stream) {
+  return mok_moe_backward_select(dims, w, x, dY, saved, nullptr, nullptr, topk_idx, topk_w, offsets,
+                                 sorted_tok, sorted_w, inv_pos, dlogits_aux, dX, dW_gate, dW_up, dW_down,
+                                 dWs_gate, dWs_up, dWs_down, dlogits, dW_router, ws, ws_bytes, stream);
+}
+
+int mok_moe_backward_select(const mok_dims* dims, const mok_weights* w, const void* x, const void* dY,
+                            const void* saved, const mok_selection* sel, const float* logits,
+                            const int32_t* topk_idx, const float* topk_w, const int32_t* offsets,
+                            const int32_t* sorted_tok, const float* sorted_w, const int32_t* inv_pos,
+                            const float* dlogits_aux, void* dX, void* dW_gate, void* dW_up,
+                            void* dW_down, void* dWs_gate, void* dWs_up, void* dWs_down, float* dlogits,
+                            void* dW_router, void* ws, size_t ws_bytes, mok_stream_t stream) {
   int rc = check_dims(dims);
+  if (rc == MOK_OK && sel) rc = check_selection(dims, sel);
   if (rc != MOK_OK) return rc;
+  if (sel && dims->T > 0 && !logits) return MOK_ERR_INVALID_ARG;
+  if (sel && (!aligned16(logits) || !aligned16(dlogits))) return MOK_ERR_UNSUPPORTED;
   if (dims->dtype == MOK_NVFP4) return MOK_ERR_UNSUPPORTED;  // the NVFP4 variant is forward only
   if (!w || !ws || !dW_gate || !dW_up || !dW_down) return MOK_ERR_INVALID_ARG;
   if (dims->T > 0 && (!x || !dY || !saved || !topk_idx || !topk_w || !offsets || !sorted_tok ||
@@ -1216,7 +1233,7 @@ int mok_moe_backward_aux(const mok_dims* dims, const mok_weights* w, const void*
     if (F % 256 || (sh && Fs % 256)) return MOK_ERR_UNSUPPORTED;  // 256-column tiles along F
     // the token-axis quantiser numbers its 128 x 64 tiles (x and dY) in an int
     if (2 * mx_nkb_routed(dims) * (d / 64) > 0x7fffffffLL) return MOK_ERR_UNSUPPORTED;
-    rc = backward_mxfp8(dims, w, x, dY, saved, topk_idx, topk_w, offsets, sorted_tok, sorted_w,
+    rc = backward_mxfp8(dims, w, x, dY, saved, sel, logits, topk_idx, topk_w, offsets, sorted_tok, sorted_w,
                         inv_pos, dlogits_aux, dX, dW_gate, dW_up, dW_down, dWs_gate, dWs_up, dWs_down, dlogits,
                         dW_router, ws, s, &launches);
     if (rc == MOK_OK) g_last_launches = launches;
@@ -1279,8 +1296,10 @@ int mok_moe_backward_aux(const mok_dims* dims, const mok_weights* w, const void*
     ++launches;
   }
   // 3. router backward: dw, dlogits, bf16 copy of dlogits
-  rc = cuda_status(launch_router_backward(T, E, dims->k, F / bn_da, topk_idx, topk_w, inv_pos, P,
-                                          dlogits_aux, dlogits, dl, s));
+  rc = cuda_status(sel ? launch_select_backward(dims, sel, logits, topk_idx, nullptr, P, inv_pos, F / bn_da,
+                                                dlogits_aux, dlogits, dl, static_cast<int*>(ws), s)
+                       : launch_router_backward(T, E, dims->k, F / bn_da, topk_idx, topk_w, inv_pos, P,
+                                                dlogits_aux, dlogits, dl, s));
   if (rc != MOK_OK) return rc;
   ++launches;
   // 4. dX_s = dG W_gate^T + dU W_up^T; shared rows also take dl W_router^T

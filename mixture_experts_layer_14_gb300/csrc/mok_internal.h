@@ -179,6 +179,14 @@ cudaError_t launch_router_backward(int64_t T, int E, int k, int ldp, const int32
                                    const float* partial, const float* aux, float* dlogits,
                                    void* dl_bf16, cudaStream_t s);
 
+// Selection (select.cu): dlogits (and its bf16 copy [T, E rounded up to 64], or NULL) from dw[T,k],
+// or where that is NULL from the partial sums <a, h> of every destination row.
+int check_selection(const mok_dims* dims, const mok_selection* sel);
+cudaError_t launch_select_backward(const mok_dims* dims, const mok_selection* sel, const float* logits,
+                                   const int32_t* topk_idx, const float* dw, const float* partial,
+                                   const int32_t* inv_pos, int ldp, const float* aux, float* dlogits,
+                                   void* dl_bf16, int* status, cudaStream_t s);
+
 // MOK_OK when the layer's sizes meet the preconditions of mok.h (api.cu).
 int check_dims(const mok_dims* d);
 
