@@ -4,13 +4,17 @@
 //   experts by their largest c or the sum of their two largest;  top-k of c in the groups that stay;
 //   w_j = scale s_j / sum s_i (or scale s_j).
 //
-// A warp takes a token, a lane a run of neighbouring experts of one group, so that among equal keys
-// the first lane and slot hold the lowest index.  Which of two experts is chosen is decided as in
-// exact arithmetic: keys are ranked in fp32, and where two that the choice depends on are nearer
-// than fp32 can tell (about one token in a thousand) the few experts in question are ranked again
-// in 64 bits.  Without a bias scores rise with the logits, which are ranked themselves.
+// A warp takes a token, a lane a run of neighbouring experts of one group, in ascending order.  The
+// k-th largest of the lanes' own largest keys is a lower limit of the k-th key, which leaves about
+// k + 2 candidates (their expected number, 32 (H(32) - H(32 - k)), is 9.1 for k = 8); these go
+// to a lane each and are ranked by counting.  Which of two experts is chosen is decided as in exact
+// arithmetic: where two keys that the choice depends on are nearer than fp32 can tell (a few tokens
+// in a thousand) the experts in question are ranked again in 64 bits.  Without a bias scores rise
+// with the logits, which are ranked themselves.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "mok_vec.cuh"
 
@@ -31,55 +35,97 @@ struct SelectParams {
   int groups, kept, n;     // groups, how many stay, experts of one
   int lanes, log_lanes;    // of a group: a power of two
   int chunk;               // experts of a lane
-  int softmax, top2, renorm;
+  int top2, renorm;
   float scale;
 };
 
-// Order-preserving unsigned image of a float; 0 and 1 stay free below the image of -inf.
-__device__ __forceinline__ unsigned ordered(float v) {
-  const unsigned b = __float_as_uint(v + 0.0f);  // -0 ranks as 0
-  return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float unordered(unsigned u) {
-  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
-}
-constexpr unsigned kAbsent = 0, kMasked = 1;  // no such expert, or its group is out; shut off
+// Keys: kAbsent for a slot without an expert, or whose group is out; kMasked for one that is shut off.
+constexpr float kAbsent = -INFINITY, kMasked = -FLT_MAX;
 // Logits and biases from here on down (-inf, the lowest value of a type) shut an expert off; sums of
 // two biases within +-1e30 stay finite.
 constexpr float kShutOff = -1e30f;
+
+__device__ __forceinline__ float warp_top(float v) {  // not NaN
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 // l - top for the exponent: 0 for the largest, whatever it is.
 template <class F>
 __device__ __forceinline__ F below(F l, F top) { return l == top ? F(0) : l - top; }
 
-// 1 / (1 + e^-l), within 2^-20 of itself (expf and the quotient 2 ulp each, the sum half of one).
-__device__ __forceinline__ float sigmoid_near(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+// e^x from one product and ex2.approx (2 ulp; results below 2^-126 are 0): off by at most
+// 2^-22 + 2^-23 |x| of itself.
+__device__ __forceinline__ float exp_near(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504f));
+  return r;
+}
+__device__ __forceinline__ float reciprocal_near(float x) {  // 1 ulp; 0 above 2^126
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
-// A token's keys in 64 bits.
-struct ExactRow {
-  const float* logits;  // of the token
-  const float* bias;    // or NULL
-  double top, sum;      // softmax: largest logit and sum of exp(l - top); sum 1 without a bias
-  bool softmax;
+// A token's row and what its scores need.
+template <bool SOFTMAX, bool BIAS>
+struct SelectRow {
+  const float* logits;
+  const float* bias;
+  float top, inv;  // softmax: largest logit, 1 / sum of exp(l - top) (1 without a bias: a common factor)
+  // Off by at most error() before the sum with the bias is rounded.
+  __device__ __forceinline__ float score(float l) const {
+    return SOFTMAX ? exp_near(below(l, top)) * inv : reciprocal_near(1.0f + exp_near(-l));
+  }
+  // The largest error of the row's scores: |x| e^-x < 0.37 for x > 0, so the errors are a multiple of
+  // the largest score; for sigmoid scores of negative logits |x| reaches the largest logit's.  softmax:
+  // the sum of at most 512 terms adds 37 roundings and the terms' own errors.
+  __device__ __forceinline__ float error() const {
+    return score(top) * (SOFTMAX ? 0x1p-17f : fmaf(0x1p-22f, fmaxf(-top, 0.0f), 0x1p-20f)) + 1e-37f;
+  }
+  __device__ __forceinline__ float open_bias(int e) const {
+    if constexpr (!BIAS) return 0.0f;
+    const float b = bias[e];
+    return fabsf(b) < -kShutOff ? b : -INFINITY;
+  }
+  // What experts are ranked by, and what groups are.
+  __device__ __forceinline__ float key(float l, float b) const {
+    return l > kShutOff ? (BIAS ? fmaxf(score(l) + b, kMasked) : l) : kMasked;
+  }
+  __device__ __forceinline__ float group_key(float l, float b) const { return l > kShutOff ? score(l) + b : -INFINITY; }
 };
-__device__ __forceinline__ double exact_key(const ExactRow& r, int e, unsigned u) {
-  if (u == kMasked) return -1e300;
+
+// Key of expert e in 64 bits; sum: of exp(l - top), for softmax with a bias.
+template <bool SOFTMAX, bool BIAS>
+__device__ __forceinline__ double exact_key(const SelectRow<SOFTMAX, BIAS>& r, double sum, int e, float key) {
+  if (key == kMasked) return -1e300;
   const double l = r.logits[e];
-  const double s = r.softmax ? exp(below(l, r.top)) / r.sum : 1.0 / (1.0 + exp(-l));
-  return r.bias ? s + (double)r.bias[e] : s;
+  const double s = SOFTMAX ? exp(below(l, (double)r.top)) / sum : 1.0 / (1.0 + exp(-l));
+  return BIAS ? s + (double)r.bias[e] : s;
+}
+template <bool SOFTMAX, bool BIAS>
+__device__ __noinline__ double exact_sum(SelectRow<SOFTMAX, BIAS> r, int E) {
+  if (!SOFTMAX || !BIAS) return 1.0;
+  double z = 0.0;
+  for (int e = threadIdx.x & 31; e < E; e += 32)
+    if (r.logits[e] > kShutOff) z += exp(below((double)r.logits[e], (double)r.top));
+  for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
+  return z;
 }
 
 // The k best experts of [lo, hi) in exact order among those with keys[e] >= threshold (k <= 8);
 // lane j < k returns the j-th (index -1: there is none).  `list` holds hi - lo numbers.  The
 // candidates are packed 24 to a round beside the best so far, so that the usual handful takes one
 // evaluation in 64 bits.
-__device__ __noinline__ int exact_best(const ExactRow& r, const unsigned* keys, int* list, int lo, int hi,
-                                       unsigned threshold, int k, double* key_out) {
+template <bool SOFTMAX, bool BIAS>
+__device__ __noinline__ int exact_best(SelectRow<SOFTMAX, BIAS> r, double sum, const float* keys, int* list, int lo, int hi,
+                                       float threshold, int k, double* key_out) {
   const int lane = threadIdx.x & 31;
   int count = 0;
   for (int e0 = lo; e0 < hi; e0 += 32) {
     const int e = e0 + lane;
-    const bool cand = e < hi && keys[e] >= threshold;
+    const bool cand = e < hi && keys[e] > kAbsent && keys[e] >= threshold;
     const unsigned mask = __ballot_sync(kAll, cand);
     if (cand) list[count + __popc(mask & ((1u << lane) - 1u))] = e;
     count += __popc(mask);
@@ -90,7 +136,7 @@ __device__ __noinline__ int exact_best(const ExactRow& r, const unsigned* keys, 
   for (int at = 0; at < count; at += 24) {
     if (lane >= 8) {
       idx = at + lane - 8 < count ? list[at + lane - 8] : -1;
-      if (idx >= 0) key = exact_key(r, idx, keys[idx]);
+      if (idx >= 0) key = exact_key(r, sum, idx, keys[idx]);
     }
     int mine = -1;
     double mine_key = 0.0;
@@ -114,20 +160,44 @@ __device__ __noinline__ int exact_best(const ExactRow& r, const unsigned* keys, 
   return idx;
 }
 
-// Sum of exp(l - top) over a token's experts, in 64 bits.
-__device__ __noinline__ double exact_sum(const float* row, int E, float top) {
-  double z = 0.0;
-  for (int e = threadIdx.x & 31; e < E; e += 32)
-    if (row[e] > kShutOff) z += exp(below((double)row[e], (double)top));
-  for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
-  return z;
+// Whether this lane's group stays, where fp32 scores of one that stays and one that goes are within
+// slack: groups farther than that from both keep their fp32 score, the others get exact ones.
+template <bool SOFTMAX, bool BIAS>
+__device__ __noinline__ bool exact_groups(SelectRow<SOFTMAX, BIAS> r, const SelectParams& p, float* keys, int* list, float err,
+                                          float score, float second, float in, float out, float slack) {
+  const int lane = threadIdx.x & 31, group = lane >> p.log_lanes;
+  for (int e = lane; e < p.E; e += 32) keys[e] = r.group_key(r.logits[e], r.open_bias(e));
+  const double sum = exact_sum(r, p.E);
+  __syncwarp();
+  double mine = score > -INFINITY ? (double)score : -1e300;
+  for (int g = 0; g < p.groups; ++g) {
+    const float sc = __shfl_sync(kAll, score, g << p.log_lanes), low = __shfl_sync(kAll, second, g << p.log_lanes);
+    if (!(sc > -INFINITY) || sc - in > slack || out - sc > slack) continue;
+    double key;
+    const int e = exact_best(r, sum, keys, list, g * p.n, (g + 1) * p.n, low - 2.0f * err - 0x1p-22f * fabsf(low),
+                             p.top2 ? 2 : 1, &key);
+    const double k1 = __shfl_sync(kAll, key, 0), k2 = __shfl_sync(kAll, key, 1);
+    const int e2 = __shfl_sync(kAll, e, 1);
+    if (group == g) mine = p.top2 && e2 >= 0 ? k1 + k2 : k1;
+  }
+  int rank = 0;
+  for (int g = 0; g < p.groups; ++g) {
+    const double other = __shfl_sync(kAll, mine, g << p.log_lanes);
+    rank += other > mine || (other == mine && g < group);
+  }
+  return rank < p.kept;
 }
 
+// Bound by issue: at T = 16384, E = 384, k = 8 with sigmoid scores and a bias, 24.9 us
+// (14.9 without a bias; 870 instructions per warp at 59% of the issue slots); ranking by rounds of a
+// maximum over the warp 47 us.
 // V: experts of a lane at most.  VEC: groups and runs are whole vectors of four.
-template <int V, bool VEC>
-__global__ void __launch_bounds__(32 * kSelectWarps) select_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ unsigned s_keys[kSelectWarps][kMaxE];  // only where fp32 cannot tell
+template <int V, bool VEC, bool SOFTMAX, bool BIAS>
+__global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ __align__(16) float s_keys[kSelectWarps][kMaxE];
   __shared__ int s_list[kSelectWarps][kMaxE];
+  __shared__ float s_key[kSelectWarps][kMaxK + 1];  // the chosen ones and the next, in order
+  __shared__ int s_idx[kSelectWarps][kMaxK + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kSelectWarps + warp;
   if (t >= p.T) return;
@@ -135,16 +205,18 @@ __global__ void __launch_bounds__(32 * kSelectWarps) select_kernel(const __grid_
   const float* row = p.logits + t * p.E;
   const int first = group * p.n + sub * p.chunk;  // this lane's experts: first .. first + own - 1
   const int own = group < p.groups ? max(0, min(p.chunk, p.n - sub * p.chunk)) : 0;
-  float l[V], b[V];
+  float* keys = s_keys[warp];
+  int* list = s_list[warp];
+  float c[V], b[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) { l[i] = -INFINITY; b[i] = 0.0f; }
+  for (int i = 0; i < V; ++i) { c[i] = -INFINITY; b[i] = 0.0f; }
   if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
       if (i < own) {
         const float4 q = *reinterpret_cast<const float4*>(row + first + i);
-        l[i] = q.x; l[i + 1] = q.y; l[i + 2] = q.z; l[i + 3] = q.w;
-        if (p.bias) {
+        c[i] = q.x; c[i + 1] = q.y; c[i + 2] = q.z; c[i + 3] = q.w;
+        if constexpr (BIAS) {
           const float4 a = *reinterpret_cast<const float4*>(p.bias + first + i);
           b[i] = a.x; b[i + 1] = a.y; b[i + 2] = a.z; b[i + 3] = a.w;
         }
@@ -154,189 +226,184 @@ __global__ void __launch_bounds__(32 * kSelectWarps) select_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (i < own) {
-        l[i] = row[first + i];
-        if (p.bias) b[i] = p.bias[first + i];
+        c[i] = row[first + i];
+        if (BIAS) b[i] = p.bias[first + i];
       }
     }
   }
-  // A logit that shuts its expert off becomes -inf, as does such a bias, which leaves the score.  NaN
-  // (and a bias that is too large) does so too and is reported.
   bool bad = false;
+  float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    bad |= l[i] != l[i] || !(b[i] < -kShutOff);
-    if (!(l[i] > kShutOff)) l[i] = -INFINITY;
-    if (!(fabsf(b[i]) < -kShutOff)) b[i] = -INFINITY;
+    bad |= c[i] != c[i];
+    top = fmaxf(top, c[i]);  // passes NaN by
+  }
+  if constexpr (BIAS) {
+    if (t == 0) {  // the same for every token
+#pragma unroll
+      for (int i = 0; i < V; ++i) bad |= !(b[i] < -kShutOff);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!(fabsf(b[i]) < -kShutOff)) b[i] = -INFINITY;
   }
   if (__any_sync(kAll, bad) && lane == 0) record_status(p.status, MOK_ERR_DEVICE_CHECK);
 
-  const bool scored = p.bias != nullptr || p.groups > 1;  // the choice depends on more than the logits' order
-  float top = -INFINITY, sum = 1.0f, smax = 1.0f;
-  if (p.softmax && (scored || !p.renorm)) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
-    top = warp_max(top);
+  SelectRow<SOFTMAX, BIAS> r{row, p.bias, warp_top(top), 1.0f};
+  float sum = 1.0f;
+  if (SOFTMAX && (BIAS || !p.renorm)) {
     float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) a += l[i] > -INFINITY ? expf(below(l[i], top)) : 0.0f;
+    for (int i = 0; i < V; ++i) a += c[i] > kShutOff ? exp_near(below(c[i], r.top)) : 0.0f;
     sum = warp_sum(a);
+    if (BIAS) r.inv = 1.0f / sum;
   }
-  unsigned u[V];
-  float err = 0.0f;  // of a key, its last rounding apart
-  if (!scored) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) u[i] = i >= own ? kAbsent : l[i] > -INFINITY ? ordered(l[i]) : kMasked;
-  } else {
-    float c[V];
-    float m = 0.0f;
-    const float inv = p.softmax && p.bias ? 1.0f / sum : 1.0f;  // without a bias a common factor changes nothing
+  const float err = r.error();
+  bool stays = true;
+  if (p.groups > 1) {
+    float t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float s = !(l[i] > -INFINITY) ? 0.0f : p.softmax ? expf(below(l[i], top)) * inv : sigmoid_near(l[i]);
-      m = fmaxf(m, s);
-      c[i] = l[i] > -INFINITY ? s + b[i] : -INFINITY;  // -inf: shut off
+      const float g = r.group_key(c[i], b[i]);  // -inf where there is no expert
+      t2 = fmaxf(t2, fminf(t1, g));
+      t1 = fmaxf(t1, g);
     }
-    smax = warp_max(m);
-    // softmax: expf 2 ulp, its argument D e^-D half ulps, the sum of at most 512 terms 37 half ulps
-    err = smax * (p.softmax ? 0x1p-17f : 0x1p-20f) + 1e-37f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      u[i] = i >= own ? kAbsent : c[i] > -INFINITY ? ordered(p.bias ? c[i] : l[i]) : kMasked;
-    if (p.groups > 1) {
-      float t1 = -INFINITY, t2 = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (i < own) {
-          t2 = fmaxf(t2, fminf(t1, c[i]));
-          t1 = fmaxf(t1, c[i]);
-        }
-      }
-      for (int o = 1; o < p.lanes; o <<= 1) {
-        const float a1 = __shfl_xor_sync(kAll, t1, o), a2 = __shfl_xor_sync(kAll, t2, o);
-        t2 = fmaxf(fmaxf(t2, a2), fminf(t1, a1));
-        t1 = fmaxf(t1, a1);
-      }
-      const float score = p.top2 && t2 > -INFINITY ? t1 + t2 : t1;
-      int rank = 0;
-      float in = INFINITY, out = -INFINITY;  // lowest score that stays, highest that goes
-      for (int g = 0; g < p.groups; ++g) {
-        const float other = __shfl_sync(kAll, score, g << p.log_lanes);
-        rank += other > score || (other == score && g < group);
-      }
-      bool stays = rank < p.kept;
-      if (group < p.groups) {
-        if (stays) in = score;
-        else out = score;
-      }
-      in = -warp_max(-in);
-      out = warp_max(out);
-      // a group without experts (-inf) never comes near one that has some
-      const float size = warp_max(t2 > -INFINITY ? fabsf(t1) + fabsf(t2) : t1 > -INFINITY ? fabsf(t1) : 0.0f);
+    for (int o = 1; o < p.lanes; o <<= 1) {
+      const float a1 = __shfl_xor_sync(kAll, t1, o), a2 = __shfl_xor_sync(kAll, t2, o);
+      t2 = fmaxf(fmaxf(t2, a2), fminf(t1, a1));
+      t1 = fmaxf(t1, a1);
+    }
+    const bool both = p.top2 && t2 > -INFINITY;
+    const float score = both ? t1 + t2 : t1;
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const float other = __shfl_sync(kAll, score, g << p.log_lanes);
+      rank += other > score || (other == score && g < group);
+    }
+    stays = rank < p.kept;
+    const bool real = group < p.groups;
+    const float in = -warp_top(real && stays ? -score : -INFINITY);   // the lowest score that stays
+    const float out = warp_top(real && !stays ? score : -INFINITY);   // the highest that goes
+    if (out > -INFINITY) {
+      const float size = warp_top(both ? fabsf(t1) + fabsf(t2) : t1 > -INFINITY ? fabsf(t1) : 0.0f);
       const float slack = 4.0f * err + 0x1p-21f * size;
-      if (p.kept < p.groups && out > -INFINITY && !(in - out > slack)) {
-        const ExactRow xr{row, p.bias, top, p.softmax && p.bias ? exact_sum(row, p.E, top) : 1.0, (bool)p.softmax};
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i < own) s_keys[warp][first + i] = c[i] > -INFINITY ? ordered(c[i]) : kAbsent;
-        __syncwarp();
-        double mine = -1e300;  // exact score of this lane's group; far ones keep their fp32 score
-        if (score > -INFINITY) mine = score;
-        for (int g = 0; g < p.groups; ++g) {
-          const float sc = __shfl_sync(kAll, score, g << p.log_lanes);
-          const float second = __shfl_sync(kAll, p.top2 && t2 > -INFINITY ? t2 : t1, g << p.log_lanes);
-          if (!(sc > -INFINITY) || sc - in > slack || out - sc > slack) continue;
-          double key;
-          const int e = exact_best(xr, s_keys[warp], s_list[warp], g * p.n, (g + 1) * p.n,
-                                   ordered(second - 2.0f * err - 0x1p-22f * fabsf(second)), p.top2 ? 2 : 1, &key);
-          const double k1 = __shfl_sync(kAll, key, 0), k2 = __shfl_sync(kAll, key, 1);
-          const int e2 = __shfl_sync(kAll, e, 1);
-          if (group == g) mine = p.top2 && e2 >= 0 ? k1 + k2 : k1;
-        }
-        rank = 0;
-        for (int g = 0; g < p.groups; ++g) {
-          const double other = __shfl_sync(kAll, mine, g << p.log_lanes);
-          rank += other > mine || (other == mine && g < group);
-        }
-        stays = rank < p.kept;
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (!stays) u[i] = kAbsent;
+      if (!(in - out > slack)) stays = exact_groups(r, p, keys, list, err, score, both ? t2 : t1, in, out, slack);
     }
   }
-
-  unsigned best = 0;
+  float best = kAbsent;
 #pragma unroll
-  for (int i = 0; i < V; ++i) best = max(best, u[i]);
-  int idx = 0;             // lane j < k: the j-th expert
-  unsigned key = kMasked;  // and its key
-  const int rounds = p.bias ? p.k + 1 : p.k;  // one more: the best of those that are not chosen
-  unsigned gone = 0;       // this lane's slots that are taken
-  for (int j = 0; j < rounds; ++j) {
-    const unsigned m = __reduce_max_sync(kAll, best);
-    const int w = __ffs(__ballot_sync(kAll, best == m)) - 1;
-    int slot = 0;
-    if (lane == w) {
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i)
-        if (u[i] == m && !(gone >> i & 1)) slot = i;
-      gone |= 1u << slot;
-      best = 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (!(gone >> i & 1)) best = max(best, u[i]);
-    }
-    const int e = __shfl_sync(kAll, first + slot, w);
-    if (lane == j) { idx = e; key = m; }
+  for (int i = 0; i < V; ++i) {
+    c[i] = i < own && stays ? r.key(c[i], b[i]) : kAbsent;
+    best = fmaxf(best, c[i]);
   }
-  if (p.bias) {
+  // The `want`-th largest of the lanes' largest keys (one more than k where the next one matters).
+  const int want = BIAS ? p.k + 1 : p.k;
+  float limit = kAbsent;
+  for (int j = 0; j < want; ++j) {
+    limit = warp_top(best);
+    const unsigned at = __ballot_sync(kAll, best == limit);
+    if (lane == __ffs(at) - 1) best = kAbsent;
+  }
+  // Candidates in ascending order: keys at the limit or above, all of them where there are fewer lanes
+  // than wanted.  Beyond 32 of them, of those at the limit the first `want`, behind the others.
+  unsigned mine = 0, equal = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine |= (c[i] >= limit && c[i] > kAbsent ? 1u : 0u) << i;
+  auto scan = [&](unsigned v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned u = __shfl_up_sync(kAll, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  unsigned upto = scan(__popc(mine));
+  int n = (int)__shfl_sync(kAll, upto, 31);
+  int at = (int)upto - __popc(mine);
+  if (n > 32) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) equal |= (c[i] == limit && c[i] > kAbsent ? 1u : 0u) << i;
+    mine &= ~equal;
+    const unsigned two = __popc(mine) | __popc(equal) << 16;
+    upto = scan(two);
+    const unsigned all = __shfl_sync(kAll, upto, 31);
+    const int more = (int)(all & 0xffff);
+    at = (int)((upto - two) & 0xffff);
+    n = more + min((int)(all >> 16), want);
+    for (int q = more + (int)((upto - two) >> 16); equal && q < n; ++q, equal &= equal - 1) list[q] = first + __ffs(equal) - 1;
+  }
+  for (; mine; mine &= mine - 1) list[at++] = first + __ffs(mine) - 1;
+  __syncwarp();
+  // A lane per candidate: its key once more, then its place in the order.
+  for (int q = lane; q < (n + 3) / 4 * 4; q += 32)
+    keys[q] = q < n ? r.key(row[list[q]], r.open_bias(list[q])) : kAbsent;
+  __syncwarp();
+  for (int q = lane; q < n; q += 32) {
+    const float key = keys[q];
+    int place = 0;
+    for (int j = 0; j < n; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(keys + j);
+      place += o.x > key || (o.x == key && j < q);
+      place += o.y > key || (o.y == key && j + 1 < q);
+      place += o.z > key || (o.z == key && j + 2 < q);
+      place += o.w > key || (o.w == key && j + 3 < q);
+    }
+    if (place < want) {
+      s_key[warp][place] = key;
+      s_idx[warp][place] = list[q];
+    }
+  }
+  __syncwarp();
+  int idx = lane < min(want, n) ? s_idx[warp][lane] : 0;  // n >= k
+  const float key = lane < min(want, n) ? s_key[warp][lane] : kAbsent;
+  if constexpr (BIAS) {
     // Neighbours in the order that are nearer than their errors, unless they are one and the same
     // number; such a pair at the border may have others as near behind it.
-    const float a = unordered(key);
-    const float last = __shfl_sync(kAll, a, p.k - 1);
+    const float last = __shfl_sync(kAll, key, p.k - 1);
+    const int last_idx = __shfl_sync(kAll, idx, p.k - 1);
     auto near = [&](float x, float y) { return !(x - y > 2.0f * err + 0x1p-23f * (fabsf(x) + fabsf(y))); };
-    const unsigned next = __shfl_down_sync(kAll, key, 1);
+    const float next = __shfl_down_sync(kAll, key, 1);
     const int other = __shfl_down_sync(kAll, idx, 1);
     bool unsure = false, tie = false;
-    if (lane < p.k && key > kMasked && next > kMasked && near(a, unordered(next))) {
+    if (lane < p.k && key > kMasked && next > kMasked && near(key, next)) {
       tie = row[idx] == row[other] && p.bias[idx] == p.bias[other];
       unsure = !tie;
     }
     if (__shfl_sync(kAll, (int)tie, p.k - 1)) {
-      const int e = __shfl_sync(kAll, idx, p.k - 1);
-      const float le = row[e], be = p.bias[e];
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        unsure |= u[i] > kMasked && !(gone >> i & 1) && near(last, unordered(u[i])) && !(l[i] == le && b[i] == be);
+#pragma unroll 1
+      for (int e = first; e < first + own; ++e) {
+        const float y = r.key(row[e], r.open_bias(e));
+        unsure |= stays && y > kMasked && (y < last || (y == last && e > last_idx)) && near(last, y) &&
+                  !(row[e] == row[last_idx] && p.bias[e] == p.bias[last_idx]);
+      }
     }
     if (__any_sync(kAll, unsure)) {
-      const ExactRow xr{row, p.bias, top, p.softmax ? exact_sum(row, p.E, top) : 1.0, (bool)p.softmax};
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i < own) s_keys[warp][first + i] = u[i];
+        if (i < own) keys[first + i] = c[i];
+      const double total = exact_sum(r, p.E);
       __syncwarp();
-      const bool all = __shfl_sync(kAll, key, p.k - 1) == kMasked;  // fewer than k are open
       double d;
-      idx = exact_best(xr, s_keys[warp], s_list[warp], 0, p.E,
-                       all ? kMasked : max(ordered(last - 2.0f * err - 0x1p-22f * fabsf(last)), kMasked), p.k, &d);
+      // kMasked: fewer than k are open
+      idx = exact_best(r, total, keys, list, 0, p.E,
+                       last == kMasked ? kMasked : fmaxf(last - 2.0f * err - 0x1p-22f * fabsf(last), kMasked), p.k, &d);
     }
   }
   // weights: lane j has its own logit
-  const bool mine = lane < p.k;
-  const float lj = mine ? row[idx] : -INFINITY;
-  const bool on = mine && lj > kShutOff;
+  const float lj = lane < p.k ? row[idx] : -INFINITY;
+  const bool on = lj > kShutOff;
   float wj = 0.0f;
   if (p.renorm) {
     // both scores over their largest possible common factor, so that small ones do not vanish:
     // softmax e^(l - m); sigmoid e^(l - m) / (1 + e^l) for m = max l <= 0, else its value
-    const float m = warp_max(on ? lj : -INFINITY);
-    if (on) wj = p.softmax ? expf(below(lj, m)) : m <= 0.0f ? expf(below(lj, m)) / (1.0f + expf(lj)) : 1.0f / (1.0f + expf(-lj));
+    const float m = warp_top(on ? lj : -INFINITY);
+    if (on) wj = SOFTMAX ? expf(below(lj, m)) : m <= 0.0f ? __fdividef(expf(below(lj, m)), 1.0f + expf(lj)) : __fdividef(1.0f, 1.0f + expf(-lj));
     const float total = warp_sum(wj);
-    wj = total > 0.0f ? p.scale * (wj / total) : 0.0f;
+    wj = total > 0.0f ? p.scale * __fdividef(wj, total) : 0.0f;
   } else if (on) {
-    wj = p.scale * (p.softmax ? expf(below(lj, top)) / sum : 1.0f / (1.0f + expf(-lj)));
+    wj = p.scale * (SOFTMAX ? __fdividef(expf(below(lj, r.top)), sum) : __fdividef(1.0f, 1.0f + expf(-lj)));
   }
-  if (mine) {
+  if (lane < p.k) {
     p.topk_idx[t * p.k + lane] = idx;
     p.topk_w[t * p.k + lane] = wj;
   }
@@ -504,7 +571,7 @@ int mok_select_experts(const mok_dims* dims, const mok_selection* sel, const flo
   set_last_launches(0);
   if (dims->T == 0) return MOK_OK;
   SelectParams p{logits, sel_bias, topk_idx, topk_w, static_cast<int*>(ws), dims->T, dims->E, dims->k, sel->n_groups,
-                 sel->topk_groups, dims->E / sel->n_groups, 1, 0, 0, sel->score == MOK_SCORE_SOFTMAX,
+                 sel->topk_groups, dims->E / sel->n_groups, 1, 0, 0,
                  sel->group_score == MOK_GROUP_TOP2, sel->renormalise != 0, sel->scale};
   while (2 * p.lanes * p.groups <= 32) {
     p.lanes *= 2;
@@ -514,9 +581,15 @@ int mok_select_experts(const mok_dims* dims, const mok_selection* sel, const flo
   const bool vec = p.n % 4 == 0;
   if (vec) p.chunk = (p.chunk + 3) / 4 * 4;
   void (*k)(const SelectParams) = nullptr;
-  if (vec) k = p.chunk <= 4 ? select_kernel<4, true> : p.chunk <= 8 ? select_kernel<8, true> : p.chunk <= 12 ? select_kernel<12, true>
-               : p.chunk <= 16 ? select_kernel<16, true> : select_kernel<32, true>;
-  else k = p.chunk <= 8 ? select_kernel<8, false> : select_kernel<32, false>;
+  auto pick = [&](auto softmax, auto bias) {
+    constexpr bool S = decltype(softmax)::value, B = decltype(bias)::value;
+    k = !vec ? select_kernel<32, false, S, B> : p.chunk <= 8 ? select_kernel<8, true, S, B> : p.chunk <= 12 ? select_kernel<12, true, S, B>
+        : p.chunk <= 16 ? select_kernel<16, true, S, B> : select_kernel<32, true, S, B>;
+  };
+  if (sel->score == MOK_SCORE_SOFTMAX && sel_bias) pick(std::true_type{}, std::true_type{});
+  else if (sel->score == MOK_SCORE_SOFTMAX) pick(std::true_type{}, std::false_type{});
+  else if (sel_bias) pick(std::false_type{}, std::true_type{});
+  else pick(std::false_type{}, std::false_type{});
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   prof_begin("select", s);
   k<<<(unsigned)((dims->T + kSelectWarps - 1) / kSelectWarps), 32 * kSelectWarps, 0, s>>>(p);
