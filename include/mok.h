@@ -454,6 +454,57 @@ int mok_moe_backward_select(const mok_dims *dims, const mok_weights *w, const vo
                             float *dlogits, void *dW_router, void *ws, size_t ws_bytes,
                             mok_stream_t stream);
 
+/* The parameters of mok_sandwich_norm and of its backward pass. */
+typedef struct {
+  float eps;               /* of both norms, > 0 */
+  float res_scale;         /* factor of the residual */
+  int32_t res_type;        /* mok_elem of residual, residual_out, h, dres and dresidual */
+  int32_t post_type, gate_type, weight_type; /* mok_elem */
+  const void *post_weight; /* [d]: the norm after the branch */
+  const void *gate;        /* [d], by channel, or NULL (1) */
+  const float *token_gate; /* [T], by token, or NULL (1) */
+  const void *weight;      /* [d]: the next norm, or NULL (none) */
+} mok_sandwich;
+
+/* The norm after a branch, its gate, the scaled residual and the next norm, in one pass per row of
+ * d elements, everything in fp32:
+ *   h = res_scale residual + token_gate gate post_weight x / sqrt(mean(x^2) + eps),
+ *   v = h / sqrt(mean(h^2) + eps) weight.
+ *   x[T,d] bf16, residual[T,d] of res_type
+ *   -> residual_out[T,d] = h in res_type; with weight: y[T,d] = v in bf16 (NULL to skip) and, with
+ *      codes, the MXFP8 form of v as in mok_rms_norm (at least one of the two); with x_codes,
+ *      x_scales, h_codes, h_scales (all or none) what the backward pass reads in 8 bits: the MXFP8
+ *      forms of x and of h (before its rounding to res_type), codes[T,d] and scales[T,d/32].
+ * residual_out may be residual, y may be x.  T >= 0, 0 < d <= 32768, d % 8 == 0 (d % 128 == 0 with
+ * codes of any kind); 16-byte aligned pointers (token_gate 4).  One launch. */
+int mok_sandwich_norm(const mok_sandwich *args, int64_t T, int d, const void *x,
+                      const void *residual, void *residual_out, void *y, void *codes, void *scales,
+                      int scale_layout, void *x_codes, void *x_scales, void *h_codes,
+                      void *h_scales, mok_stream_t stream);
+
+/* Bytes of workspace of mok_sandwich_norm_backward (0 for invalid sizes). */
+size_t mok_sandwich_norm_workspace_size(int64_t T, int d);
+
+/* Gradients of mok_sandwich_norm.  With rho1, rho2 the reciprocal roots, xhat = x rho1, hhat = h rho2
+ * (recomputed), W = post_weight gate and g = dy weight:
+ *   ds = rho2 (g - hhat mean(g hhat)) + dres,  dresidual = res_scale ds,
+ *   dx = rho1 token_gate (ds W - xhat mean(ds W xhat)),  dtoken_gate[t] = sum ds W xhat,
+ *   dpost_weight = gate A, dgate = post_weight A with A = sum over rows of token_gate ds xhat,
+ *   dweight = sum over rows of dy hhat (rows in a fixed order).
+ *   dy[T,d] bf16 (with weight, else NULL), dres[T,d] of res_type (the gradient that arrives through
+ *   residual_out) or NULL: at least one.  x[T,d] bf16 and h[T,d] of res_type (residual_out; NULL
+ *   without weight), or with x_scales and h_scales [T,d/32] their MXFP8 forms as the forward pass
+ *   wrote them: the gradients are then those at the values that these hold.
+ *   -> dx[T,d] bf16, dresidual[T,d] of res_type, dpost_weight[d], dgate[d] (with gate),
+ *      dtoken_gate[T] (with token_gate), dweight[d] (with weight) fp32.
+ * dx may be dy, dresidual may be dres.  Sizes and alignment as in mok_sandwich_norm.  Two launches,
+ * the second begins under the first. */
+int mok_sandwich_norm_backward(const mok_sandwich *args, int64_t T, int d, const void *dy,
+                               const void *dres, const void *x, const void *x_scales, const void *h,
+                               const void *h_scales, void *dx, void *dresidual, float *dpost_weight,
+                               float *dgate, float *dtoken_gate, float *dweight, void *ws,
+                               size_t ws_bytes, mok_stream_t stream);
+
 /* Schedule of the bf16 expert GEMMs of mok_moe_forward (process-wide; default
  * MOK_SCHEDULE_TWO_LAUNCHES):
  *  - MOK_SCHEDULE_TWO_LAUNCHES: gate/up + SwiGLU, then down + router weight, each one persistent

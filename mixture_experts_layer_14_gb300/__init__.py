@@ -24,7 +24,8 @@ __all__ = [
     "mx_quantize_rows", "nvfp4_set_activation_amax",
     "rms_norm", "rms_norm_backward", "rms_norm_workspace_size", "balance_loss",
     "balance_loss_workspace_size", "TensorList", "grad_norm", "grad_norm_workspace_size", "AdamW",
-    "MoEBlock", "Selection", "select_experts", "select_experts_backward",
+    "MoEBlock", "Selection", "select_experts", "select_experts_backward", "sandwich_norm",
+    "sandwich_norm_backward", "sandwich_norm_workspace_size",
 ]
 
 MOK_BF16, MOK_MXFP8, MOK_NVFP4 = 0, 1, 2
@@ -42,6 +43,7 @@ EXPORTED_SYMBOLS = [
     "mok_balance_loss_workspace_size", "mok_balance_loss", "mok_grad_norm_workspace_size",
     "mok_grad_norm", "mok_adamw_step", "mok_moe_forward_mx", "mok_moe_backward_aux",
     "mok_select_experts", "mok_select_experts_backward", "mok_moe_backward_select",
+    "mok_sandwich_norm", "mok_sandwich_norm_workspace_size", "mok_sandwich_norm_backward",
 ]
 
 
@@ -89,6 +91,12 @@ class Selection(ctypes.Structure):
             raise ValueError("scoring must be 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
         super().__init__(self.SCORES[scoring], n_groups, topk_groups, self.GROUP_SCORES[group_score],
                          bool(renormalise), scale)
+
+
+class Sandwich(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("res_scale", ctypes.c_float)] + [
+        (n, ctypes.c_int32) for n in ("res_type", "post_type", "gate_type", "weight_type")] + [
+        (n, ctypes.c_void_p) for n in ("post_weight", "gate", "token_gate", "weight")]
 
 
 _LIB = None
@@ -148,6 +156,9 @@ def lib():
             "mok_select_experts": (ctypes.c_int, [_DP, _SP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
             "mok_select_experts_backward": (ctypes.c_int, [_DP, _SP] + [_VP] * 6 + [_SZ, _VP]),
             "mok_moe_backward_select": (ctypes.c_int, [_DP, _WP] + [_VP] * 3 + [_SP] + [_VP] * 18 + [_SZ, _VP]),
+            "mok_sandwich_norm": (ctypes.c_int, [ctypes.POINTER(Sandwich), _I64, _INT] + [_VP] * 6 + [_INT] + [_VP] * 5),
+            "mok_sandwich_norm_workspace_size": (_SZ, [_I64, _INT]),
+            "mok_sandwich_norm_backward": (ctypes.c_int, [ctypes.POINTER(Sandwich), _I64, _INT] + [_VP] * 13 + [_SZ, _VP]),
             "mok_timing_collect": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_int),
                                                   ctypes.POINTER(ctypes.c_double), ctypes.c_int,
                                                   ctypes.POINTER(ctypes.c_int)]),
@@ -178,6 +189,13 @@ def _stream():
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _stream_of(dev):
+    """The current stream of the tensors' device, which has to be the current one."""
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors live on {dev}, not on the current device cuda:{torch.cuda.current_device()}")
+    return _stream()
 
 
 def _want(t, name, shape, dtype, device, check_device=True):
@@ -454,6 +472,123 @@ def rms_norm_backward(dy, s, weight, eps=1e-6, dres=None, ws=None):
     return out
 
 
+def _sandwich(shape, dev, kind, post_weight, weight, gate, token_gate, res_scale, eps):
+    T, d = shape
+    _want(post_weight, "post_weight", (d,), post_weight.dtype, dev)
+    for t, name in ((weight, "weight"), (gate, "gate")):
+        if t is not None:
+            _want(t, name, (d,), t.dtype, dev)
+    if token_gate is not None:
+        _want(token_gate, "token_gate", (T,), torch.float32, dev)
+    return Sandwich(eps, res_scale, kind, _elem(post_weight, "post_weight"), 0 if gate is None else _elem(gate, "gate"),
+                    0 if weight is None else _elem(weight, "weight"), post_weight.data_ptr(), _ptr(gate),
+                    _ptr(token_gate), _ptr(weight))
+
+
+def sandwich_norm(x, residual, post_weight, weight=None, gate=None, token_gate=None, res_scale=1.0, eps=1e-6, mx=None,
+                  want_y=True, save=None):
+    """The norm after a branch with its gate, the scaled residual and the next norm in one pass over
+    the rows of x [T,d] bf16 and residual [T,d] (bf16 or fp32), in fp32:
+    h = res_scale residual + token_gate gate post_weight x / sqrt(mean(x^2) + eps),
+    v = h / sqrt(mean(h^2) + eps) weight.  post_weight, weight and gate [d] are bf16 or fp32,
+    token_gate [T] fp32; weight None: no next norm.  Returns a dict: "residual" (h in residual's type)
+    and, with weight, "y" (v in bf16; not with want_y=False) and with mx="rows" or "atoms" its MXFP8
+    form as in :func:`rms_norm`.  save="mxfp8": also what the backward pass reads in 8 bits,
+    "x_codes", "x_scales", "h_codes", "h_scales" (uint8 [T,d] and [T,d/32])."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    shape, dev = x.shape, x.device
+    T, d = shape
+    _want(x, "x", shape, torch.bfloat16, dev)
+    kind = _elem(residual, "residual")
+    _want(residual, "residual", shape, residual.dtype, dev)
+    a = _sandwich(shape, dev, kind, post_weight, weight, gate, token_gate, res_scale, eps)
+    if mx not in (None, "rows", "atoms") or save not in (None, "mxfp8"):
+        raise ValueError("mx must be None, 'rows' or 'atoms', save None or 'mxfp8'")
+    if mx is not None and weight is None:
+        raise ValueError("mx needs weight")
+    out = {"residual": torch.empty_like(residual)}
+    if weight is not None and want_y:
+        out["y"] = torch.empty_like(x)
+    if mx is not None:
+        out["codes"] = torch.empty(shape, dtype=torch.uint8, device=dev)
+        out["scales"] = torch.empty((T, d // 32) if mx == "rows" else (_scale_bytes(T, d, mx),), dtype=torch.uint8,
+                                    device=dev)
+    if save is not None:
+        for k in ("x", "h"):
+            out[k + "_codes"] = torch.empty(shape, dtype=torch.uint8, device=dev)
+            out[k + "_scales"] = torch.empty((T, d // 32), dtype=torch.uint8, device=dev)
+    get = out.get
+    _check(lib().mok_sandwich_norm(
+        ctypes.byref(a), T, d, x.data_ptr(), residual.data_ptr(), out["residual"].data_ptr(), _ptr(get("y")),
+        _ptr(get("codes")), _ptr(get("scales")), 1 if mx == "atoms" else 0, _ptr(get("x_codes")), _ptr(get("x_scales")),
+        _ptr(get("h_codes")), _ptr(get("h_scales")), _stream_of(dev)))
+    return out
+
+
+def sandwich_norm_workspace_size(T, d):
+    n = lib().mok_sandwich_norm_workspace_size(T, d)
+    if n == 0:
+        raise MokError("unsupported norm dimensions")
+    return n
+
+
+def sandwich_norm_backward(x, h, post_weight, dy=None, dres=None, weight=None, gate=None, token_gate=None,
+                           res_scale=1.0, eps=1e-6, residual_dtype=None, ws=None):
+    """Gradients of :func:`sandwich_norm`: dy [T,d] bf16 of "y" (with weight), dres [T,d] of
+    "residual", in its type, or None.  x and h are the forward pass's x and "residual", or each a
+    tuple (codes, scales) of its 8-bit form; h None without weight.  ``residual_dtype``: the residual's
+    type where neither h nor dres tells it (default bf16).  Returns a dict: "dx" [T,d] bf16,
+    "dresidual" [T,d] in the residual's type, fp32 "dpost_weight" [d] and, for those given, "dweight"
+    [d], "dgate" [d], "dtoken_gate" [T].  ``ws``: at least sandwich_norm_workspace_size(T, d) bytes
+    (allocated per call when None)."""
+    packed = isinstance(x, tuple)
+    rows, x_scales = x if packed else (x, None)
+    if rows.dim() != 2:
+        raise ValueError("x must be 2-D")
+    shape, dev = rows.shape, rows.device
+    T, d = shape
+    if (dy is None) != (weight is None) or (dy is not None and h is None):
+        raise ValueError("weight needs dy and h, and dy needs weight")
+    if dy is None and dres is None:
+        raise ValueError("dy or dres is required")
+    if h is not None and isinstance(h, tuple) != packed:
+        raise ValueError("x and h must both be tensors or both codes and scales")
+    h_rows, h_scales = h if packed and h is not None else (h, None)
+    if dy is None:
+        h_rows = h_scales = None
+    kind = dres.dtype if dres is not None else h_rows.dtype if h_rows is not None and not packed else (
+        residual_dtype or torch.bfloat16)
+    if kind not in _ELEM or (residual_dtype is not None and residual_dtype != kind):
+        raise ValueError(f"the residual's dtype {kind} is not as given, or neither bfloat16 nor float32")
+    _want(rows, "x", shape, torch.uint8 if packed else torch.bfloat16, dev)
+    if packed:
+        _want(x_scales, "x scales", (T, d // 32), torch.uint8, dev)
+    if dy is not None:
+        _want(dy, "dy", shape, torch.bfloat16, dev)
+        _want(h_rows, "h", shape, torch.uint8 if packed else kind, dev)
+        if packed:
+            _want(h_scales, "h scales", (T, d // 32), torch.uint8, dev)
+    if dres is not None:
+        _want(dres, "dres", shape, kind, dev)
+    a = _sandwich(shape, dev, _ELEM[kind], post_weight, weight, gate, token_gate, res_scale, eps)
+    if ws is None:
+        ws = torch.empty(sandwich_norm_workspace_size(T, d), dtype=torch.uint8, device=dev)
+    _want_ws(ws, dev)
+    out = {"dx": torch.empty(shape, dtype=torch.bfloat16, device=dev),
+           "dresidual": torch.empty(shape, dtype=kind, device=dev),
+           "dpost_weight": torch.empty((d,), dtype=torch.float32, device=dev)}
+    for t, name, n in ((weight, "dweight", d), (gate, "dgate", d), (token_gate, "dtoken_gate", T)):
+        if t is not None:
+            out[name] = torch.empty((n,), dtype=torch.float32, device=dev)
+    get = out.get
+    _check(lib().mok_sandwich_norm_backward(
+        ctypes.byref(a), T, d, _ptr(dy), _ptr(dres), rows.data_ptr(), _ptr(x_scales), _ptr(h_rows), _ptr(h_scales),
+        out["dx"].data_ptr(), out["dresidual"].data_ptr(), out["dpost_weight"].data_ptr(), _ptr(get("dgate")),
+        _ptr(get("dtoken_gate")), _ptr(get("dweight")), ws.data_ptr(), ws.numel(), _stream_of(dev)))
+    return out
+
+
 def balance_loss_workspace_size(D, n_seqs=1):
     n = lib().mok_balance_loss_workspace_size(ctypes.byref(D), n_seqs)
     if n == 0:
@@ -508,7 +643,7 @@ def select_experts(D, sel, logits, ws, bias=None):
     idx = torch.empty((D.T, D.k), dtype=torch.int32, device=dev)
     w = torch.empty((D.T, D.k), dtype=torch.float32, device=dev)
     _check(lib().mok_select_experts(ctypes.byref(D), ctypes.byref(sel), logits.data_ptr(), _ptr(bias), idx.data_ptr(),
-                                    w.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
+                                    w.data_ptr(), ws.data_ptr(), ws.numel(), _stream_of(dev)))
     return idx, w
 
 
@@ -526,7 +661,7 @@ def select_experts_backward(D, sel, logits, topk_idx, dtopk_w, ws, dlogits_aux=N
     dlogits = torch.empty_like(logits)
     _check(lib().mok_select_experts_backward(
         ctypes.byref(D), ctypes.byref(sel), logits.data_ptr(), topk_idx.data_ptr(), dtopk_w.data_ptr(),
-        _ptr(dlogits_aux), dlogits.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
+        _ptr(dlogits_aux), dlogits.data_ptr(), ws.data_ptr(), ws.numel(), _stream_of(dev)))
     return dlogits
 
 

@@ -1,0 +1,87 @@
+// Rows of bf16 or fp32 elements, eight at a time: raw vectors, a ring of rows in shared memory that a
+// thread fills by asynchronous copies of exactly what it reads back itself, and pairs for the
+// two-wide fp32 instructions.  Used by the norms.
+#pragma once
+
+#include "mok_mx.cuh"
+#include "mok_vec.cuh"
+
+namespace mok {
+
+// Eight elements as they are stored: bf16 in one register quadruple, fp32 in two.
+template <bool F32>
+struct Raw8 {
+  uint4 u[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> raw8(const void* p, int64_t i) {
+  Raw8<F32> r;
+  if constexpr (F32) {
+    r.u[0] = static_cast<const uint4*>(p)[2 * i];
+    r.u[1] = static_cast<const uint4*>(p)[2 * i + 1];
+  } else {
+    r.u[0] = static_cast<const uint4*>(p)[i];
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> zero8() {
+  Raw8<F32> r;
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) r.u[i] = make_uint4(0, 0, 0, 0);
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ Vec8 value8(const Raw8<F32>& r) {
+  if constexpr (F32)
+    return {__uint_as_float(r.u[0].x), __uint_as_float(r.u[0].y), __uint_as_float(r.u[0].z), __uint_as_float(r.u[0].w),
+            __uint_as_float(r.u[1].x), __uint_as_float(r.u[1].y), __uint_as_float(r.u[1].z), __uint_as_float(r.u[1].w)};
+  else
+    return unpack8(r.u[0]);
+}
+
+// Vector v of a row that begins at vector `row` of the array, to the ring's place `at` (bytes): bf16
+// in one plane of 16 bytes per vector; fp32 in two, through L1, because each copy uses half a
+// sector (past L1, or with the halves of a warp's vectors redistributed, 10-25% slower).
+template <bool F32>
+__device__ __forceinline__ void copy8(uint32_t at, const void* p, int64_t row, int v, int nvec) {
+  if (v >= nvec) return;
+  if constexpr (F32) {
+    copy16_ca(at + 16 * v, static_cast<const uint4*>(p) + 2 * (row + v));
+    copy16_ca(at + 16 * (nvec + v), static_cast<const uint4*>(p) + 2 * (row + v) + 1);
+  } else {
+    copy16(at + 16 * v, static_cast<const uint4*>(p) + row + v);
+  }
+}
+__device__ __forceinline__ uint4 ring16(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at));
+  return u;
+}
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> ring8(uint32_t at, int v, int nvec) {
+  Raw8<F32> r;
+  r.u[0] = ring16(at + 16 * v);
+  if constexpr (F32) r.u[1] = ring16(at + 16 * (nvec + v));
+  return r;
+}
+__device__ __forceinline__ Vec8 load_weight(const void* w, int f32, int v, bool in) {
+  if (!in) return {};
+  return f32 ? load8<true>(w, v) : load8<false>(w, v);
+}
+
+// Eight values as four pairs, for the two-wide fp32 instructions: with scalar ones the RMS
+// norm's backward pass takes 360 instructions per warp and row, three quarters of the issue slots.
+struct Pairs {
+  float2 p[4];
+};
+__device__ __forceinline__ Pairs pairs(const Vec8& a) {
+  Pairs r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r.p[j] = make_float2(a.v[2 * j], a.v[2 * j + 1]);
+  return r;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+
+}  // namespace mok

@@ -65,3 +65,32 @@ def select_grad(logits, idx, dw, scoring, renorm=True, scale=1.0):
         for j, v in zip(ok, g):
             out[t, idx[t, j]] += v
     return out
+
+
+def sandwich(x, r, post, weight=None, gate=None, token_gate=None, a=1.0, eps=1e-6):
+    """(h, v)."""
+    n = x / np.sqrt((x * x).mean(1, keepdims=True) + eps) * post
+    n = n * (1.0 if gate is None else gate) * (1.0 if token_gate is None else token_gate[:, None])
+    h = a * r + n
+    return h, None if weight is None else h / np.sqrt((h * h).mean(1, keepdims=True) + eps) * weight
+
+
+def sandwich_grad(x, h, post, dy=None, dres=None, weight=None, gate=None, token_gate=None, a=1.0, eps=1e-6):
+    out, ds = {}, np.zeros_like(x) if dres is None else dres
+    if dy is not None:
+        rho = 1.0 / np.sqrt((h * h).mean(1, keepdims=True) + eps)
+        hhat, g = h * rho, dy * weight
+        ds = ds + rho * (g - hhat * (g * hhat).mean(1, keepdims=True))
+        out["dweight"] = (dy * hhat).sum(0)
+    W = post if gate is None else post * gate
+    t = np.ones((len(x), 1)) if token_gate is None else token_gate[:, None]
+    rho = 1.0 / np.sqrt((x * x).mean(1, keepdims=True) + eps)
+    xhat, gw = x * rho, ds * W
+    A = (t * ds * xhat).sum(0)
+    out.update(dx=rho * t * (gw - xhat * (gw * xhat).mean(1, keepdims=True)), dresidual=a * ds,
+               dpost_weight=A * (1.0 if gate is None else gate))
+    if gate is not None:
+        out["dgate"] = A * post
+    if token_gate is not None:
+        out["dtoken_gate"] = (gw * xhat).sum(1)
+    return out

@@ -85,3 +85,71 @@ def test_selection_binding():
             mok.select_experts(D, mok.Selection(), *args)
     with pytest.raises(ValueError):
         mok.select_experts_backward(D, mok.Selection(), l, torch.zeros(4, 2), torch.zeros(4, 2), torch.zeros(256))
+
+
+def _args(**kw):
+    a = dict(eps=1e-6, res_scale=1.0, res_type=0, post_type=0, gate_type=0, weight_type=0, post_weight=P, gate=NULL,
+             token_gate=NULL, weight=P)
+    a.update({k: v for k, v in kw.items() if k in a})
+    return mok.Sandwich(**a), {k: v for k, v in kw.items() if k not in a}
+
+
+def _sandwich(T=4, d=256, null=False, **kw):
+    a, kw = _args(**kw)
+    p = dict(x=P, r=P, ro=P, y=P, q=NULL, sc=NULL, layout=0, xq=NULL, xs=NULL, hq=NULL, hs=NULL)
+    p.update(kw)
+    return ensure_lib().mok_sandwich_norm(None if null else ctypes.byref(a), T, d, *p.values(), NULL)
+
+
+PARAMS = [(dict(null=True), INVALID), (dict(T=-1), UNSUPPORTED), (dict(d=0), UNSUPPORTED), (dict(d=12), UNSUPPORTED),
+          (dict(d=32776), UNSUPPORTED), (dict(eps=0.0), INVALID), (dict(eps=float("nan")), INVALID),
+          (dict(res_scale=float("inf")), INVALID), (dict(res_type=2), INVALID), (dict(post_type=-1), INVALID),
+          (dict(gate_type=2), INVALID), (dict(weight_type=3), INVALID), (dict(post_weight=NULL), INVALID),
+          (dict(post_weight=ODD), UNSUPPORTED), (dict(weight=ODD), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("kw,rc", PARAMS + [
+    (dict(gate=ODD), UNSUPPORTED), (dict(token_gate=ODD4), UNSUPPORTED),
+    (dict(d=64, q=P, sc=P), UNSUPPORTED), (dict(d=64, xq=P, xs=P, hq=P, hs=P), UNSUPPORTED), (dict(x=NULL), INVALID),
+    (dict(r=NULL), INVALID), (dict(ro=NULL), INVALID), (dict(y=NULL), INVALID), (dict(weight=NULL), INVALID),
+    (dict(weight=NULL, y=NULL, q=P, sc=P), INVALID), (dict(q=P), INVALID), (dict(sc=P), INVALID), (dict(layout=2), INVALID),
+    (dict(xq=P), INVALID), (dict(xq=P, xs=P, hq=P), INVALID), (dict(x=ODD), UNSUPPORTED), (dict(ro=ODD), UNSUPPORTED),
+    (dict(y=ODD), UNSUPPORTED), (dict(q=P, sc=ODD), UNSUPPORTED), (dict(xq=P, xs=P, hq=ODD, hs=P), UNSUPPORTED)])
+def test_sandwich_norm(kw, rc):
+    assert _sandwich(**kw) == rc
+
+
+def _sandwich_bwd(T=4, d=256, null=False, n=1 << 30, **kw):
+    a, kw = _args(**kw)
+    p = dict(dy=P, dres=P, x=P, xs=NULL, h=P, hs=NULL, dx=P, dr=P, dpost=P, dgate=NULL, dtg=NULL, dw=P, ws=P)
+    p.update(kw)
+    return ensure_lib().mok_sandwich_norm_backward(None if null else ctypes.byref(a), T, d, *p.values(), n, NULL)
+
+
+@pytest.mark.parametrize("kw,rc", PARAMS + [
+    (dict(gate=ODD, dgate=P), UNSUPPORTED), (dict(token_gate=ODD4, dtg=P), UNSUPPORTED), (dict(token_gate=P, dtg=ODD4), UNSUPPORTED),
+    (dict(gate=P), INVALID), (dict(dgate=P), INVALID), (dict(token_gate=P), INVALID), (dict(dtg=P), INVALID),
+    (dict(weight=NULL), INVALID), (dict(weight=NULL, dw=NULL), INVALID), (dict(dw=NULL), INVALID), (dict(dy=NULL), INVALID),
+    (dict(h=NULL), INVALID), (dict(x=NULL), INVALID), (dict(dx=NULL), INVALID), (dict(dr=NULL), INVALID),
+    (dict(dpost=NULL), INVALID), (dict(ws=NULL), INVALID), (dict(dy=NULL, weight=NULL, dw=NULL, dres=NULL), INVALID),
+    (dict(xs=P), INVALID), (dict(hs=P), INVALID), (dict(d=64, xs=P, hs=P), UNSUPPORTED), (dict(dres=ODD), UNSUPPORTED),
+    (dict(xs=ODD, hs=P), UNSUPPORTED), (dict(dx=ODD), UNSUPPORTED), (dict(dpost=ODD), UNSUPPORTED), (dict(n=64), WORKSPACE)])
+def test_sandwich_norm_backward(kw, rc):
+    assert _sandwich_bwd(**kw) == rc
+
+
+def test_sandwich_binding():
+    x, w = torch.zeros(4, 256, dtype=torch.bfloat16), torch.ones(256)
+    c = (torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(4, 8, dtype=torch.uint8))
+    assert ensure_lib().mok_sandwich_norm_workspace_size(4, 12) == 0
+    assert mok.sandwich_norm_workspace_size(4, 256) >= 256 + 8 * 256
+    for bad in (dict(x=x[0]), dict(x=x.float()), dict(residual=x[:2]), dict(residual=x.half()), dict(post_weight=w[1:]),
+                dict(weight=w.double()), dict(gate=w[:3]), dict(token_gate=w), dict(mx="rows", weight=None), dict(mx="cols"),
+                dict(save="int8"), dict()):                                   # the last: not on a GPU
+        with pytest.raises(ValueError):
+            mok.sandwich_norm(**dict(dict(x=x, residual=x, post_weight=w, weight=w), **bad))
+    for bad in (dict(dy=None), dict(weight=None), dict(h=None), dict(dy=None, weight=None), dict(x=c), dict(h=c),
+                dict(residual_dtype=torch.float32), dict(dres=x.float()), dict(x=(c[0], c[1][:2]), h=c), dict(x=c, h=c,
+                residual_dtype=torch.float16), dict(x=x[0]), dict()):
+        with pytest.raises(ValueError):
+            mok.sandwich_norm_backward(**dict(dict(x=x, h=x, post_weight=w, dy=x, weight=w), **bad))

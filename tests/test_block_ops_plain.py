@@ -43,3 +43,31 @@ def test_selection_rules():
     l[0, :7] = -np.inf
     idx, w = _block.select(l, 3, "softmax")
     assert idx.tolist() == [[7, 0, 1]] and w.tolist() == [[1.0, 0.0, 0.0]]
+
+
+@pytest.mark.parametrize("next_norm,gated", [(True, True), (True, False), (False, True)])
+def test_sandwich_gradient_against_differences(next_norm, gated):
+    rng = np.random.default_rng(4)
+    T, d = 3, 8
+    v = dict(x=rng.normal(size=(T, d)), r=rng.normal(size=(T, d)), post=rng.normal(size=d))
+    if next_norm:
+        v["weight"] = rng.normal(size=d)
+    if gated:
+        v["gate"], v["token_gate"] = rng.normal(size=d), rng.normal(size=T)
+    dh, dv = rng.normal(size=(T, d)), rng.normal(size=(T, d))
+
+    def loss(**kw):
+        h, y = _block.sandwich(**kw, a=0.7)
+        return (h * dh).sum() + (0.0 if y is None else (y * dv).sum())
+
+    h, _ = _block.sandwich(**v, a=0.7)
+    rest = {k: v[k] for k in ("weight", "gate", "token_gate") if k in v}
+    g = _block.sandwich_grad(v["x"], h, v["post"], dv if next_norm else None, dh, a=0.7, **rest)
+    names = dict(x="dx", r="dresidual", post="dpost_weight", weight="dweight", gate="dgate", token_gate="dtoken_gate")
+    for k in v:
+        for i in np.ndindex(v[k].shape):
+            lo, hi = v[k].copy(), v[k].copy()
+            lo[i] -= 1e-5
+            hi[i] += 1e-5
+            diff = (loss(**dict(v, **{k: hi})) - loss(**dict(v, **{k: lo}))) / 2e-5
+            assert abs(diff - g[names[k]][i]) < 1e-7
