@@ -505,6 +505,29 @@ int mok_sandwich_norm_backward(const mok_sandwich *args, int64_t T, int d, const
                                float *dgate, float *dtoken_gate, float *dweight, void *ws,
                                size_t ws_bytes, mok_stream_t stream);
 
+/* Activations in 8 bits and back, for what a training step keeps between its passes: src[rows,K] of
+ * type (mok_elem) -> codes[rows,K] E4M3 and scales[rows,K/32] UE8M0 by the rule of
+ * mok_mx_quantize_rows (NaN stays NaN, its block's scale is that of the others), and codes times scales
+ * -> dst[rows,K] of type, exact but where it leaves the type's range (a scale byte 255 is NaN);
+ * scale_layout: that of the scales read.  rows >= 0, K % 32 == 0 (K % 128 == 0 with scale atoms),
+ * rows * K <= 2^40; 16-byte aligned pointers.  One launch each. */
+int mok_activation_pack(int64_t rows, int K, const void *src, int type, void *codes, void *scales,
+                        mok_stream_t stream);
+int mok_activation_unpack(int64_t rows, int K, const void *codes, const void *scales,
+                          int scale_layout, void *dst, int type, mok_stream_t stream);
+
+/* What mok_moe_forward saved for the backward pass, in 8 bits: `packed` (mok_packed_saved_size bytes;
+ * 0 for dims without a backward pass) receives G and U of the routed rows and of the shared expert as
+ * mok_activation_pack gives them; x in expert order, which `saved` also holds for MOK_BF16, is left
+ * out.  mok_saved_unpack fills `saved` again, from `packed` and (MOK_BF16) from x[T,d] by inv_pos, for
+ * mok_moe_backward with the same routing: `saved` may serve many layers in turn.  At the
+ * DeepSeek-V3 training shape (T = 8192, d = 7168, k = 8, F = Fs = 2048) 0.31 GB are kept per layer in
+ * place of 1.54 GB (bf16) or 1.21 GB (MXFP8).  One launch; mok_saved_unpack two for MOK_BF16. */
+size_t mok_packed_saved_size(const mok_dims *dims);
+int mok_saved_pack(const mok_dims *dims, const void *saved, void *packed, mok_stream_t stream);
+int mok_saved_unpack(const mok_dims *dims, const void *packed, const void *x,
+                     const int32_t *inv_pos, void *saved, mok_stream_t stream);
+
 /* Schedule of the bf16 expert GEMMs of mok_moe_forward (process-wide; default
  * MOK_SCHEDULE_TWO_LAUNCHES):
  *  - MOK_SCHEDULE_TWO_LAUNCHES: gate/up + SwiGLU, then down + router weight, each one persistent

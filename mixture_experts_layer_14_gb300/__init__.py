@@ -25,7 +25,8 @@ __all__ = [
     "rms_norm", "rms_norm_backward", "rms_norm_workspace_size", "balance_loss",
     "balance_loss_workspace_size", "TensorList", "grad_norm", "grad_norm_workspace_size", "AdamW",
     "MoEBlock", "Selection", "select_experts", "select_experts_backward", "sandwich_norm",
-    "sandwich_norm_backward", "sandwich_norm_workspace_size",
+    "sandwich_norm_backward", "sandwich_norm_workspace_size", "activation_pack", "activation_unpack",
+    "saved_pack", "saved_unpack",
 ]
 
 MOK_BF16, MOK_MXFP8, MOK_NVFP4 = 0, 1, 2
@@ -44,6 +45,7 @@ EXPORTED_SYMBOLS = [
     "mok_grad_norm", "mok_adamw_step", "mok_moe_forward_mx", "mok_moe_backward_aux",
     "mok_select_experts", "mok_select_experts_backward", "mok_moe_backward_select",
     "mok_sandwich_norm", "mok_sandwich_norm_workspace_size", "mok_sandwich_norm_backward",
+    "mok_activation_pack", "mok_activation_unpack", "mok_packed_saved_size", "mok_saved_pack", "mok_saved_unpack",
 ]
 
 
@@ -159,6 +161,11 @@ def lib():
             "mok_sandwich_norm": (ctypes.c_int, [ctypes.POINTER(Sandwich), _I64, _INT] + [_VP] * 6 + [_INT] + [_VP] * 5),
             "mok_sandwich_norm_workspace_size": (_SZ, [_I64, _INT]),
             "mok_sandwich_norm_backward": (ctypes.c_int, [ctypes.POINTER(Sandwich), _I64, _INT] + [_VP] * 13 + [_SZ, _VP]),
+            "mok_activation_pack": (ctypes.c_int, [_I64, _INT, _VP, _INT, _VP, _VP, _VP]),
+            "mok_activation_unpack": (ctypes.c_int, [_I64, _INT, _VP, _VP, _INT, _VP, _INT, _VP]),
+            "mok_packed_saved_size": (_SZ, [_DP]),
+            "mok_saved_pack": (ctypes.c_int, [_DP, _VP, _VP, _VP]),
+            "mok_saved_unpack": (ctypes.c_int, [_DP] + [_VP] * 5),
             "mok_timing_collect": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_int),
                                                   ctypes.POINTER(ctypes.c_double), ctypes.c_int,
                                                   ctypes.POINTER(ctypes.c_int)]),
@@ -665,6 +672,64 @@ def select_experts_backward(D, sel, logits, topk_idx, dtopk_w, ws, dlogits_aux=N
     return dlogits
 
 
+def activation_pack(x):
+    """An activation [..., K] bf16 or fp32 in 8 bits: (codes uint8 of x's shape, scales uint8
+    [..., K/32]), E4M3 values and one UE8M0 scale per 32 elements by the rule of
+    :func:`mx_quantize_rows`."""
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x must have a last dimension")
+    kind, K = _elem(x, "x"), x.shape[-1]
+    _want(x, "x", x.shape, x.dtype, None)
+    codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    scales = torch.empty(x.shape[:-1] + (K // 32,), dtype=torch.uint8, device=x.device)
+    _check(lib().mok_activation_pack(x.numel() // K, K, x.data_ptr(), kind, codes.data_ptr(), scales.data_ptr(),
+                                     _stream_of(x.device)))
+    return codes, scales
+
+
+def activation_unpack(codes, scales, dtype=torch.bfloat16, layout="rows", out=None):
+    """The activation [..., K] in ``dtype`` (bf16 or fp32) that codes and scales of
+    :func:`activation_pack` hold; layout "atoms": scales in the atoms of ``rms_norm(mx="atoms")``, for
+    codes [T,d].  ``out``: where to, or None."""
+    if codes.dim() < 1 or codes.shape[-1] == 0:
+        raise ValueError("codes must have a last dimension")
+    if layout not in ("rows", "atoms") or dtype not in _ELEM:
+        raise ValueError("layout must be 'rows' or 'atoms', dtype bfloat16 or float32")
+    shape, dev, K = codes.shape, codes.device, codes.shape[-1]
+    rows = codes.numel() // K
+    _want(codes, "codes", shape, torch.uint8, None)
+    _want(scales, "scales", shape[:-1] + (K // 32,) if layout == "rows" else (_scale_bytes(rows, K, layout),),
+          torch.uint8, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    _want(out, "out", shape, dtype, dev)
+    _check(lib().mok_activation_unpack(rows, K, codes.data_ptr(), scales.data_ptr(), 1 if layout == "atoms" else 0,
+                                       out.data_ptr(), _ELEM[dtype], _stream_of(dev)))
+    return out
+
+
+def saved_pack(D, saved):
+    """The 8-bit form (uint8) of what :func:`moe_forward` wrote into ``saved``, which is then free for
+    another layer until :func:`saved_unpack`."""
+    _want(saved, "saved", (saved_size(D),), torch.uint8, None)
+    packed = torch.empty(lib().mok_packed_saved_size(ctypes.byref(D)), dtype=torch.uint8, device=saved.device)
+    _check(lib().mok_saved_pack(ctypes.byref(D), saved.data_ptr(), packed.data_ptr(), _stream_of(saved.device)))
+    return packed
+
+
+def saved_unpack(D, packed, x, routing, saved):
+    """Fills ``saved`` from its 8-bit form, and for bf16 layers from the layer's input x [T,d] and its
+    routing, for :func:`moe_backward`."""
+    dev = saved.device
+    _want(saved, "saved", (saved_size(D),), torch.uint8, None)
+    _want(packed, "packed", (lib().mok_packed_saved_size(ctypes.byref(D)),), torch.uint8, dev)
+    _want(x, "x", (D.T, D.d), torch.bfloat16, dev)
+    _want(routing["inv_pos"], "inv_pos", (D.T, D.k), torch.int32, dev)
+    _check(lib().mok_saved_unpack(ctypes.byref(D), packed.data_ptr(), x.data_ptr(), routing["inv_pos"].data_ptr(),
+                                  saved.data_ptr(), _stream_of(dev)))
+    return saved
+
+
 def prepared_size(D):
     return lib().mok_prepared_size(ctypes.byref(D))
 
@@ -787,15 +852,24 @@ class MoELayer:
     """Holds the weights of one layer and its workspaces; calls the C ABI in sequence.  ``backward``
     belongs to the last forward with training=True, whatever ran for inference since.  ``selection``
     (a :class:`Selection`): how experts are chosen from the router's logits, with the balance bias
-    W["balance_bias"] [E] fp32, if there is one; None: the softmax router of :func:`route`."""
+    W["balance_bias"] [E] fp32, if there is one; None: the softmax router of :func:`route`.
+    ``checkpoint`` "mxfp8": what the forward pass saves is kept in 8 bits, and ``saved`` (a uint8 tensor
+    of saved_size(D) bytes, allocated when None) is free between the passes, so that layers of one
+    shape that run on one stream may all be given the same."""
 
-    def __init__(self, D, W, device=None, selection=None):
+    def __init__(self, D, W, device=None, selection=None, checkpoint=None, saved=None):
+        if checkpoint not in (None, "mxfp8"):
+            raise ValueError("checkpoint must be None or 'mxfp8'")
+        if saved is not None:
+            _want(saved, "saved", (saved_size(D),), torch.uint8, W["W_gate"].device)
         self.D = D
         self.W = W
         self.selection = selection
+        self.checkpoint = checkpoint
         dev = device or W["W_gate"].device
         self.ws = torch.zeros(workspace_size(D), dtype=torch.uint8, device=dev)
-        self.saved = None
+        self.saved = saved
+        self._packed = None   # ``saved`` in 8 bits
         self._trained = None  # the routing that ``saved`` belongs to
         self._ws_bwd = None
 
@@ -811,11 +885,14 @@ class MoELayer:
         if training and self.saved is None:
             self.saved = torch.empty(saved_size(self.D), dtype=torch.uint8, device=x.device)
         if training:
-            self._trained = None
+            self._trained = self._packed = None
         y = moe_forward(self.D, self.W, x, routing, self.ws, saved=self.saved if training else None,
                         x_mx=x_mx)
         self.last_launches = n + last_launch_count()  # kernels this call enqueued
         self.routing = routing
+        if training and self.checkpoint:
+            self._packed = saved_pack(self.D, self.saved)
+            self.last_launches += last_launch_count()
         if training:
             self._trained = routing, None if self.selection is None else self.logits
         return y
@@ -827,9 +904,13 @@ class MoELayer:
             self._ws_bwd = torch.zeros(workspace_size(self.D, backward=True), dtype=torch.uint8,
                                        device=x.device)
         routing, logits = self._trained
+        n = 0
+        if self.checkpoint:
+            saved_unpack(self.D, self._packed, x, routing, self.saved)
+            n = last_launch_count()
         g = moe_backward(self.D, self.W, x, dY, self.saved, routing, self._ws_bwd, dlogits_aux=dlogits_aux,
                          selection=self.selection, logits=logits)
-        self.last_launches = last_launch_count()
+        self.last_launches = n + last_launch_count()
         return g
 
 

@@ -277,6 +277,23 @@ static Layout layout_saved(const mok_dims* d) {
   return L;
 }
 
+// `saved` in 8 bits: codes and scales of its first four slots, in turn.
+static Layout layout_packed(const mok_dims* d) {
+  const int64_t T = d->T, R = T * d->k;
+  const int Fs = d->n_shared ? d->F_shared : 0;
+  const size_t n[4] = {(size_t)R * d->F, (size_t)R * d->F, (size_t)T * Fs, (size_t)T * Fs};
+  Layout L{};
+  size_t o = 0;
+  for (int i = 0; i < 4; ++i) {
+    L.off[2 * i] = o;
+    o += al(n[i]);
+    L.off[2 * i + 1] = o;
+    o += al(n[i] / 32);
+  }
+  L.total = o;
+  return L;
+}
+
 static Layout layout_host(const mok_dims* d) {
   const int64_t T = d->T, R = T * d->k;
   // x: two buffers, alternating per call (see mok_layer_forward_host)
@@ -1160,6 +1177,57 @@ int mok_moe_forward_mx(const mok_dims* dims, const mok_weights* w, const void* x
   if (dims->T > 0 && (!x_codes || !x_scales)) return MOK_ERR_INVALID_ARG;
   return moe_forward(dims, w, nullptr, x_codes, x_scales, topk_idx, offsets, sorted_tok, sorted_w,
                      inv_pos, y, saved, ws, ws_bytes, stream);
+}
+
+size_t mok_packed_saved_size(const mok_dims* dims) {
+  if (check_dims(dims) != MOK_OK || dims->dtype == MOK_NVFP4) return 0;
+  return layout_packed(dims).total;
+}
+
+static int saved_packing(bool pack, const mok_dims* dims, void* saved, void* packed, cudaStream_t s) {
+  const Layout S = layout_saved(dims), P = layout_packed(dims);
+  const int64_t R = dims->T * dims->k, Fs = dims->n_shared ? dims->F_shared : 0;
+  const int64_t elems[4] = {R * dims->F, R * dims->F, dims->T * Fs, dims->T * Fs};
+  void* wide[4];
+  uint8_t *codes[4], *scales[4];
+  for (int i = 0; i < 4; ++i) {
+    wide[i] = at<void*>(saved, S.off[SV_G + i]);
+    codes[i] = at<uint8_t*>(packed, P.off[2 * i]);
+    scales[i] = at<uint8_t*>(packed, P.off[2 * i + 1]);
+  }
+  return cuda_status(launch_pack_segments(pack, dims->dtype == MOK_MXFP8, 4, wide, codes, scales, elems, s));
+}
+
+int mok_saved_pack(const mok_dims* dims, const void* saved, void* packed, mok_stream_t stream) {
+  int rc = check_dims(dims);
+  if (rc != MOK_OK) return rc;
+  if (dims->dtype == MOK_NVFP4) return MOK_ERR_UNSUPPORTED;
+  if (dims->T > 0 && (!saved || !packed)) return MOK_ERR_INVALID_ARG;
+  if (!aligned16(saved) || !aligned16(packed)) return MOK_ERR_UNSUPPORTED;
+  g_last_launches = 0;
+  if (dims->T == 0) return MOK_OK;
+  rc = saved_packing(true, dims, const_cast<void*>(saved), packed, reinterpret_cast<cudaStream_t>(stream));
+  if (rc == MOK_OK) g_last_launches = 1;
+  return rc;
+}
+
+int mok_saved_unpack(const mok_dims* dims, const void* packed, const void* x, const int32_t* inv_pos, void* saved,
+                     mok_stream_t stream) {
+  int rc = check_dims(dims);
+  if (rc != MOK_OK) return rc;
+  if (dims->dtype == MOK_NVFP4) return MOK_ERR_UNSUPPORTED;
+  const bool rows = dims->dtype == MOK_BF16;  // x in expert order
+  if (dims->T > 0 && (!saved || !packed || (rows && (!x || !inv_pos)))) return MOK_ERR_INVALID_ARG;
+  if (!aligned16(saved) || !aligned16(packed) || !aligned16(x)) return MOK_ERR_UNSUPPORTED;
+  g_last_launches = 0;
+  if (dims->T == 0) return MOK_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  rc = saved_packing(false, dims, saved, const_cast<void*>(packed), s);
+  if (rc == MOK_OK && rows)
+    rc = cuda_status(launch_gather_rows("gather_x", x, nullptr, inv_pos, dims->T, dims->k, 2 * dims->d,
+                                        at<void*>(saved, layout_saved(dims).off[SV_XS]), nullptr, s));
+  if (rc == MOK_OK) g_last_launches = rows ? 2 : 1;
+  return rc;
 }
 
 int mok_moe_backward(const mok_dims* dims, const mok_weights* w, const void* x, const void* dY,

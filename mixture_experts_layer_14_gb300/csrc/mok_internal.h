@@ -179,6 +179,11 @@ cudaError_t launch_router_backward(int64_t T, int E, int k, int ldp, const int32
                                    const float* partial, const float* aux, float* dlogits,
                                    void* dl_bf16, cudaStream_t s);
 
+// Packing (pack.cu): up to four tensors (empty ones are left out) between their wide form, bf16 or
+// fp32, and E4M3 codes with row-major UE8M0 scales, in one launch.
+cudaError_t launch_pack_segments(bool pack, bool f32, int segments, void* const* wide, uint8_t* const* codes,
+                                 uint8_t* const* scales, const int64_t* elems, cudaStream_t s);
+
 // Selection (select.cu): dlogits (and its bf16 copy [T, E rounded up to 64], or NULL) from dw[T,k],
 // or where that is NULL from the partial sums <a, h> of every destination row.
 int check_selection(const mok_dims* dims, const mok_selection* sel);

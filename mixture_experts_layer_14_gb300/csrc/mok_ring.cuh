@@ -1,7 +1,9 @@
 // Rows of bf16 or fp32 elements, eight at a time: raw vectors, a ring of rows in shared memory that a
 // thread fills by asynchronous copies of exactly what it reads back itself, and pairs for the
-// two-wide fp32 instructions.  Used by the norms.
+// two-wide fp32 instructions.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "mok_mx.cuh"
 #include "mok_vec.cuh"
@@ -70,6 +72,25 @@ __device__ __forceinline__ Vec8 load_weight(const void* w, int f32, int v, bool 
   return f32 ? load8<true>(w, v) : load8<false>(w, v);
 }
 
+// Values of eight E4M3 codes times their block's scale (a UE8M0 byte; every product is exact but
+// where it leaves fp32's range).
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
+}
+__device__ __forceinline__ Vec8 dequantise8(uint2 q, float scale) {
+  Vec8 r;
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t two;  // f16 pair: holds every E4M3 value
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+    r.v[2 * i] = f.x * scale;
+    r.v[2 * i + 1] = f.y * scale;
+  }
+  return r;
+}
+
 // Eight values as four pairs, for the two-wide fp32 instructions: with scalar ones the RMS
 // norm's backward pass takes 360 instructions per warp and row, three quarters of the issue slots.
 struct Pairs {
@@ -82,6 +103,5 @@ __device__ __forceinline__ Pairs pairs(const Vec8& a) {
   return r;
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
-
 
 }  // namespace mok

@@ -230,25 +230,6 @@ struct SandwichBwdParams {
   int post_f32, gate_f32, weight_f32, depth;
 };
 
-// Values of eight E4M3 codes times their block's scale (a UE8M0 byte; every product is exact but
-// where it leaves fp32's range).
-__device__ __forceinline__ float mx_scale(uint32_t byte) {
-  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
-}
-__device__ __forceinline__ Vec8 dequantise8(uint2 q, float scale) {
-  Vec8 r;
-  const uint32_t w[2] = {q.x, q.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t two;  // f16 pair: holds every E4M3 value
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
-    r.v[2 * i] = f.x * scale;
-    r.v[2 * i + 1] = f.y * scale;
-  }
-  return r;
-}
-
 // PACKED: x and h come as codes and scales.
 template <int V, bool F32, bool PACKED, bool RING, int MT>
 __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p) {

@@ -153,3 +153,54 @@ def test_sandwich_binding():
                 residual_dtype=torch.float16), dict(x=x[0]), dict()):
         with pytest.raises(ValueError):
             mok.sandwich_norm_backward(**dict(dict(x=x, h=x, post_weight=w, dy=x, weight=w), **bad))
+
+
+def _pack(rows=4, K=64, src=P, kind=0, q=P, s=P):
+    return ensure_lib().mok_activation_pack(rows, K, src, kind, q, s, NULL)
+
+
+def _unpack(rows=4, K=64, src=P, kind=0, q=P, s=P, layout=0):
+    return ensure_lib().mok_activation_unpack(rows, K, q, s, layout, src, kind, NULL)
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(rows=-1), UNSUPPORTED), (dict(K=0), UNSUPPORTED), (dict(K=48), UNSUPPORTED), (dict(rows=1 << 36), UNSUPPORTED),
+    (dict(kind=2), INVALID), (dict(src=NULL), INVALID), (dict(q=NULL), INVALID), (dict(s=NULL), INVALID),
+    (dict(src=ODD), UNSUPPORTED), (dict(q=ODD), UNSUPPORTED), (dict(s=ODD), UNSUPPORTED)])
+def test_activation_pack(kw, rc):
+    assert _pack(**kw) == rc and _unpack(**kw) == rc
+
+
+def test_activation_unpack_layouts_and_saved():
+    L = ensure_lib()
+    assert _unpack(layout=2) == INVALID and _unpack(layout=1) == UNSUPPORTED
+    assert _pack(rows=0, src=NULL, q=NULL, s=NULL) == 0 and _unpack(rows=0, src=NULL, q=NULL, s=NULL) == 0
+    D, D4 = mok.dims(16, 256, 8, 2, 256, 256, 1), mok.dims(16, 256, 8, 2, 256, 256, 1, mok.MOK_NVFP4)
+    D8, D0 = mok.dims(16, 256, 8, 2, 256, 256, 1, mok.MOK_MXFP8), mok.dims(0, 256, 8, 2, 256, 256, 1)
+    n = 2 * (32 + 16) * 256
+    assert n * 33 // 32 <= L.mok_packed_saved_size(ctypes.byref(D)) <= n * 33 // 32 + 8 * 1024
+    assert L.mok_packed_saved_size(ctypes.byref(D4)) == 0
+
+    def pack(d, saved=P, packed=P):
+        return L.mok_saved_pack(ctypes.byref(d), saved, packed, NULL)
+
+    def unpack(d, packed=P, x=P, inv=P, saved=P):
+        return L.mok_saved_unpack(ctypes.byref(d), packed, x, inv, saved, NULL)
+    assert pack(D4) == UNSUPPORTED and unpack(D4) == UNSUPPORTED
+    assert pack(D, saved=NULL) == INVALID and pack(D, packed=NULL) == INVALID and pack(D, saved=ODD) == UNSUPPORTED
+    assert unpack(D, packed=NULL) == INVALID and unpack(D, x=NULL) == INVALID and unpack(D, inv=NULL) == INVALID
+    assert unpack(D8, saved=NULL) == INVALID and unpack(D, x=ODD) == UNSUPPORTED and unpack(D, packed=ODD) == UNSUPPORTED
+    assert pack(D0, NULL, NULL) == 0 and unpack(D0, NULL, NULL, NULL, NULL) == 0
+
+
+def test_packing_binding():
+    x = torch.zeros(4, 64)
+    for bad in (x.half(), torch.zeros(()), torch.zeros(4, 0), x):                     # the last: not on a GPU
+        with pytest.raises(ValueError):
+            mok.activation_pack(bad)
+    c, s = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)
+    for args in ((c, s, torch.float16), (c, s, torch.float32, "columns"), (c.float(), s), (c, s[:2]), (c, s)):
+        with pytest.raises(ValueError):
+            mok.activation_unpack(*args)
+    with pytest.raises(ValueError):
+        mok.saved_pack(mok.dims(16, 256, 8, 2, 256, 256, 1), torch.zeros(8, dtype=torch.uint8))
