@@ -77,14 +77,21 @@ __device__ __forceinline__ Vec8 load_weight(const void* w, int f32, int v, bool 
 __device__ __forceinline__ float mx_scale(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
 }
+__device__ __forceinline__ uint4 e4m3_halves(uint2 q) {  // as f16, which holds every E4M3 value
+  uint4 r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.x) : "h"((uint16_t)q.x));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.y) : "h"((uint16_t)(q.x >> 16)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.z) : "h"((uint16_t)q.y));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.w) : "h"((uint16_t)(q.y >> 16)));
+  return r;
+}
 __device__ __forceinline__ Vec8 dequantise8(uint2 q, float scale) {
   Vec8 r;
-  const uint32_t w[2] = {q.x, q.y};
+  const uint4 u = e4m3_halves(q);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t two;  // f16 pair: holds every E4M3 value
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
     r.v[2 * i] = f.x * scale;
     r.v[2 * i + 1] = f.y * scale;
   }
@@ -103,5 +110,26 @@ __device__ __forceinline__ Pairs pairs(const Vec8& a) {
   return r;
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+template <bool F32>
+__device__ __forceinline__ void store_pairs(void* p, int64_t i, const Pairs& a) {
+  store8<F32>(p, i, {a.p[0].x, a.p[0].y, a.p[1].x, a.p[1].y, a.p[2].x, a.p[2].y, a.p[3].x, a.p[3].y});
+}
+
+// The scale byte s + 127 of a block with this largest magnitude, s the smallest integer with amax <= 448
+// 2^s = 1.75 2^(s + 8): the exponent less 8, and one more for mantissas above 1.75, which the sum
+// carries over.  (mx_exponent without its cases: subnormal numbers give 0 all the same.)
+__device__ __forceinline__ int mx_scale_byte(float amax) {
+  return max((int)((__float_as_uint(amax) + 0x1fffffu) >> 23) - 8, 0);
+}
+__device__ __forceinline__ uint2 mx_codes8(const Pairs& a, int byte) {
+  const float2 inv = both(__uint_as_float((uint32_t)(254 - byte) << 23));  // 2^-s
+  uint32_t q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = __fmul2_rn(a.p[j], inv);
+    q[j] = e4m3x2(v.x, v.y);
+  }
+  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
 
 }  // namespace mok

@@ -7,10 +7,10 @@
 //   dx = rho1 tg (ds W - xhat mean(ds W xhat)),  W = post gate,  q = sum ds W xhat = dtoken_gate,
 //   A = sum over rows of tg ds xhat:  dpost = A gate,  dgate = A post,  dweight = sum dv hhat.
 //
-// Both are bound by HBM.  A block stays for many rows, which come through a ring in shared memory by
-// asynchronous copies two rows ahead, and holds the present one in registers.  Each row needs two
-// sums of which the second follows from the first; the first ones are taken a row ahead, so that
-// both go through one exchange and one barrier per row.
+// Both are bound by HBM, and close to it by issue.  A block stays for many rows, which one thread
+// fetches into a ring in shared memory by bulk copies (whole rows are contiguous) up to three rows
+// ahead.  Each row needs two sums of which the second follows from the first; the first ones are
+// taken a row ahead, so that both go through one exchange and one barrier per row.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -42,59 +42,104 @@ struct SandwichParams {
   int post_f32, gate_f32, weight_f32, atoms, depth;
 };
 
-// Sums of N values over the row's threads, the same in all of them: a row is a block's or a warp's
-// (32 threads in x).  `turn` alternates between calls: two buffers need one barrier per call.
-template <int N, int W>
-__device__ __forceinline__ void row_sums(float (&a)[N], float (&smem)[2][W][N], int turn) {
-  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+// Sums of N = 2 or 4 values over the row's threads, the same in all of them: a row is a block's, of at most
+// 16 warps, or a warp's (32 threads in x).  While values are left a step of the tree halves their number
+// instead of adding all of them up in every lane, which takes a third of the instructions.  `turn`
+// alternates between calls: two buffers need one barrier per call.  smem is zero where there is no warp.
+template <int N>
+__device__ __forceinline__ void row_sums(float (&a)[N], float (&smem)[2][N][16], int turn) {
+  constexpr unsigned kFull = 0xffffffffu;
+  constexpr int L = 32 / N;  // lanes that share a value in the end
+  const int lane = threadIdx.x & 31, value = lane / L;
+  float v;
+  if constexpr (N == 4) {
+    const bool hi = lane & 16;
+    const float x = (hi ? a[2] : a[0]) + __shfl_xor_sync(kFull, hi ? a[0] : a[2], 16);
+    const float y = (hi ? a[3] : a[1]) + __shfl_xor_sync(kFull, hi ? a[1] : a[3], 16);
+    const bool up = lane & 8;
+    v = (up ? y : x) + __shfl_xor_sync(kFull, up ? x : y, 8);
+  } else {
+    const bool hi = lane & 16;
+    v = (hi ? a[1] : a[0]) + __shfl_xor_sync(kFull, hi ? a[0] : a[1], 16);
+  }
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
+  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  if (blockDim.x > 32) {
+    if (lane % L == 0) smem[turn][value][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = smem[turn][value][lane % L];
+    if constexpr (N == 4) v += smem[turn][value][lane % L + 8];
 #pragma unroll
-    for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
-  if (warps == 1) return;
-  if (lane == 0)
+    for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  }
 #pragma unroll
-    for (int i = 0; i < N; ++i) smem[turn][threadIdx.x >> 5][i] = a[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) a[i] = lane < warps ? smem[turn][lane][i] : 0.0f;
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+  for (int i = 0; i < N; ++i) a[i] = __shfl_sync(kFull, v, i * L);
 }
-
 // MXFP8 form of eight elements whose block of 32 lies in four neighbouring lanes.
-__device__ __forceinline__ void quantise8(const Vec8& a, bool in, void* codes, int64_t at, uint8_t* scale, bool first) {
+__device__ __forceinline__ void quantise8(const Pairs& a, bool in, void* codes, int64_t at, uint8_t* scale, bool first) {
   float amax = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(a.v[j]));
+  for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(a.p[j].x), fabsf(a.p[j].y)));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  const int s = mx_exponent(amax);
-  const float inv = __uint_as_float((uint32_t)(127 - s) << 23);
+  const int byte = mx_scale_byte(amax);
   if (!in) return;
-  uint2 q;
-  q.x = e4m3x2(a.v[0] * inv, a.v[1] * inv) | (uint32_t)e4m3x2(a.v[2] * inv, a.v[3] * inv) << 16;
-  q.y = e4m3x2(a.v[4] * inv, a.v[5] * inv) | (uint32_t)e4m3x2(a.v[6] * inv, a.v[7] * inv) << 16;
-  static_cast<uint2*>(codes)[at] = q;
-  if (first) *scale = (uint8_t)(s + 127);
+  static_cast<uint2*>(codes)[at] = mx_codes8(a, byte);
+  if (first) *scale = (uint8_t)byte;
+}
+
+// A ring of `depth` rows: each place has an mbarrier that the copies of its row complete.
+struct RowRing {
+  uint32_t base, place, bars;  // first place, bytes of one, first barrier
+  int depth, slot;
+  uint32_t phase;
+  bool ok;                     // no wait has run out (its row is then made NaN, not left to chance)
+  __device__ __forceinline__ uint32_t at(int ahead) const {  // place of the row `ahead` of the present one
+    int k = slot + ahead;
+    if (k >= depth) k -= depth;
+    return base + k * place;
+  }
+  __device__ __forceinline__ uint32_t bar(int ahead) const {
+    int k = slot + ahead;
+    if (k >= depth) k -= depth;
+    return bars + 8 * k;
+  }
+  __device__ __forceinline__ void wait(int ahead, volatile int* abort) {
+    ok &= mbar_wait(bar(ahead), slot + ahead >= depth ? phase ^ 1 : phase, nullptr, abort);
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == depth) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+template <bool F32>
+__device__ __forceinline__ Pairs row_pairs(uint32_t at, int v) {  // vector v of a row in shared memory
+  if constexpr (!F32) return pairs(unpack8(ring16(at + 16 * v)));
+  Raw8<true> r;
+  r.u[0] = ring16(at + 32 * v);
+  r.u[1] = ring16(at + 32 * v + 16);
+  return pairs(value8<true>(r));
 }
 
 // V vectors of eight per thread, MT threads at most.
 template <int V, bool F32, bool RING, int MT>
 __global__ void __launch_bounds__(MT) sandwich_kernel(const __grid_constant__ SandwichParams p) {
-  __shared__ float smem[2][32][2];
+  __shared__ float smem[2][2][16];
+  __shared__ __align__(8) uint64_t bars[8][3];
+  __shared__ int s_abort;
   extern __shared__ __align__(16) uint8_t ring[];
   const int nvec = p.d >> 3;
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
-  int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  constexpr int kPlanes = 1 + (F32 ? 2 : 1);  // of 16 bytes per vector
-  const uint32_t place = kPlanes * 16 * nvec;
-  const uint32_t base = smem_u32(ring) + threadIdx.y * p.depth * place;
+  const int step = gridDim.x * blockDim.y, T = (int)p.T;
+  int t = blockIdx.x * blockDim.y + threadIdx.y;
+  int64_t row = (int64_t)t * nvec;  // vectors before the row
+  const int64_t row_step = (int64_t)step * nvec;
+  constexpr int kRes = F32 ? 32 : 16;
   constexpr bool kHold = V <= 2;  // the weights in registers; else read where they are used
+  RowRing q{smem_u32(ring) + threadIdx.y * p.depth * (16 + kRes) * nvec, (16u + kRes) * nvec, smem_u32(bars[threadIdx.y]), p.depth, 0, 0, true};
   bool in[V];
-  Vec8 W[kHold ? V : 1], w2[kHold ? V : 1];
+  Pairs W[kHold ? V : 1], w2[kHold ? V : 1];
   auto inner = [&](int v, bool ok) {  // post gate
     Vec8 a = load_weight(p.post, p.post_f32, v, ok);
     if (p.gate) {
@@ -102,111 +147,121 @@ __global__ void __launch_bounds__(MT) sandwich_kernel(const __grid_constant__ Sa
 #pragma unroll
       for (int j = 0; j < 8; ++j) a.v[j] *= g.v[j];
     }
-    return a;
+    return pairs(a);
   };
-  auto fetch = [&](int64_t row, uint32_t at) {
-    if constexpr (!RING) return;
-    if (row < p.T) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        copy8<false>(at, p.x, row * nvec, v, nvec);
-        copy8<F32>(at + 16 * nvec, p.residual, row * nvec, v, nvec);
-      }
+  // the row `ahead` of the present one; every read of what is in its place has ended
+  auto fetch = [&](int ahead) {
+    if (RING && threadIdx.x == 0 && t + (int64_t)ahead * step < T) {
+      const int64_t from = row + ahead * row_step;
+      const uint32_t at = ahead == q.depth ? q.at(0) : q.at(ahead), bar = ahead == q.depth ? q.bar(0) : q.bar(ahead);
+      mbar_arrive_expect_tx(bar, q.place);
+      bulk_load(at, static_cast<const uint4*>(p.x) + from, 16 * nvec, bar);
+      bulk_load(at + 16 * nvec, static_cast<const char*>(p.residual) + kRes * from, kRes * nvec, bar);
     }
-    copies_end();
   };
-  auto read_x = [&](int64_t row, uint32_t at, int v) {
-    if constexpr (RING) return value8<false>(ring8<false>(at, v, nvec));
-    else return load8<false>(p.x, row * nvec + v);
+  auto read_x = [&](int64_t from, int ahead, int v) {
+    if constexpr (RING) return row_pairs<false>(q.at(ahead), v);
+    else return pairs(load8<false>(p.x, from + v));
   };
-  auto read_r = [&](int64_t row, uint32_t at, int v) {
-    if constexpr (RING) return value8<F32>(ring8<F32>(at + 16 * nvec, v, nvec));
-    else return load8<F32>(p.residual, row * nvec + v);
-  };
-  auto square_of = [&](int64_t row, uint32_t at) {  // this thread's share of sum x^2
-    float ss = 0.0f;
+  auto square_of = [&](int64_t from, int ahead) {  // this thread's share of sum x^2
+    float2 ss = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (in[i]) {
-        const Vec8 a = read_x(row, at, threadIdx.x + i * blockDim.x);
+        const Pairs a = read_x(from, ahead, threadIdx.x + i * blockDim.x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(a.v[j], a.v[j], ss);
+        for (int j = 0; j < 4; ++j) ss = __ffma2_rn(a.p[j], a.p[j], ss);
       }
     }
-    return ss;
+    return q.ok ? ss.x + ss.y : NAN;
   };
 #pragma unroll
-  for (int i = 0; i < V; ++i) in[i] = threadIdx.x + i * blockDim.x < nvec;
-  uint32_t at = base, last = base + (p.depth - 1) * place;  // this row's place, and the one before it
-  fetch(t, base);
-  fetch(t + step, base + place);
+  for (int i = 0; i < V; ++i) in[i] = i < V - 1 || threadIdx.x + i * blockDim.x < nvec;  // only the last can be past the row
+  if (RING && threadIdx.x == 0) {
+    for (int k = 0; k < p.depth; ++k) mbar_init(q.bars + 8 * k, 1);
+    if (threadIdx.y == 0) s_abort = 0;
+    fence_barrier_init();
+  }
+  if (threadIdx.y == 0)
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) (&smem[0][0][0])[i] = 0.0f;
+  __syncthreads();
+  for (int k = 0; k < p.depth; ++k) fetch(k);
   float gate = 1.0f, next_gate = 1.0f;
-  if (p.token_gate && t < p.T) gate = p.token_gate[t];
+  if (p.token_gate && t < T) gate = p.token_gate[t];
 #pragma unroll
   for (int i = 0; i < (kHold ? V : 0); ++i) {
     W[i] = inner(threadIdx.x + i * blockDim.x, in[i]);
-    w2[i] = p.weight ? load_weight(p.weight, p.weight_f32, threadIdx.x + i * blockDim.x, in[i]) : Vec8{};
+    w2[i] = pairs(p.weight ? load_weight(p.weight, p.weight_f32, threadIdx.x + i * blockDim.x, in[i]) : Vec8{});
   }
-  if constexpr (RING) copies_wait<1>();
-  float sums[2] = {0.0f, t < p.T ? square_of(t, base) : 0.0f};
+  float sums[2] = {0.0f, 0.0f};
+  if (t < T) {
+    if constexpr (RING) q.wait(0, &s_abort);
+    sums[1] = square_of(row, 0);
+  }
   row_sums(sums, smem, 1);
-  for (int turn = 0; t < p.T; t += step, turn ^= 1) {
-    fetch(t + 2 * step, last);
-    if constexpr (RING) copies_wait<1>();
-    const uint32_t next = at + place == base + p.depth * place ? base : at + place;
-    if (p.token_gate && t + step < p.T) next_gate = p.token_gate[t + step];
-    const float rho1 = rsqrtf(fmaf(sums[1], p.inv_d, p.eps)) * gate;
-    Vec8 h[V];
-    float ss = 0.0f;
+  const float2 a2 = both(p.res_scale);
+  for (int turn = 0; t < T; turn ^= 1) {
+    const bool more = t + step < T;
+    if (p.token_gate && more) next_gate = p.token_gate[t + step];
+    const float2 rho1 = both(rsqrtf(fmaf(sums[1], p.inv_d, p.eps)) * gate);
+    Pairs h[V];
+    float2 ss = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      Vec8 x{};
-      h[i] = Vec8{};
+      Pairs x{};
+      h[i] = Pairs{};
       if (in[i]) {
-        x = read_x(t, at, v);
-        h[i] = read_r(t, at, v);
-        const Vec8 w = kHold ? W[kHold ? i : 0] : inner(v, true);
+        x = read_x(row, 0, v);
+        if constexpr (RING) h[i] = row_pairs<F32>(q.at(0) + 16 * nvec, v);
+        else h[i] = pairs(load8<F32>(p.residual, row + v));
+        const Pairs w = kHold ? W[kHold ? i : 0] : inner(v, true);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[i].v[j] = fmaf(x.v[j] * rho1, w.v[j], p.res_scale * h[i].v[j]);
-          ss = fmaf(h[i].v[j], h[i].v[j], ss);
+        for (int j = 0; j < 4; ++j) {
+          h[i].p[j] = __ffma2_rn(__fmul2_rn(x.p[j], rho1), w.p[j], __fmul2_rn(h[i].p[j], a2));
+          ss = __ffma2_rn(h[i].p[j], h[i].p[j], ss);
         }
-        store8<F32>(p.residual_out, t * nvec + v, h[i]);
+        store_pairs<F32>(p.residual_out, row + v, h[i]);
       }
       if (p.x_codes) {
-        const int64_t s = t * (nvec >> 2) + (v >> 2);
-        quantise8(x, in[i], p.x_codes, t * nvec + v, p.x_scales + s, (v & 3) == 0);
-        quantise8(h[i], in[i], p.h_codes, t * nvec + v, p.h_scales + s, (v & 3) == 0);
+        const int64_t s = (row + v) >> 2;
+        quantise8(x, in[i], p.x_codes, row + v, p.x_scales + s, (v & 3) == 0);
+        quantise8(h[i], in[i], p.h_codes, row + v, p.h_scales + s, (v & 3) == 0);
       }
     }
-    sums[0] = ss;
-    sums[1] = t + step < p.T ? square_of(t + step, next) : 0.0f;
+    sums[0] = ss.x + ss.y;
+    sums[1] = 0.0f;
+    if (more) {
+      if constexpr (RING) q.wait(1, &s_abort);
+      sums[1] = square_of(row + row_step, 1);
+    }
     row_sums(sums, smem, turn);
+    if (blockDim.x == 32) __syncwarp();
+    fetch(q.depth);  // into this row's place
     if (p.weight) {
-      const float rho2 = rsqrtf(fmaf(sums[0], p.inv_d, p.eps));
+      const float2 rho2 = both(rsqrtf(fmaf(sums[0], p.inv_d, p.eps)));
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
-        const Vec8 w = kHold ? w2[kHold ? i : 0] : load_weight(p.weight, p.weight_f32, v, in[i]);
+        const Pairs w = kHold ? w2[kHold ? i : 0] : pairs(load_weight(p.weight, p.weight_f32, v, in[i]));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i].v[j] = h[i].v[j] * rho2 * w.v[j];
-        if (p.y && in[i]) store8<false>(p.y, t * nvec + v, h[i]);
+        for (int j = 0; j < 4; ++j) h[i].p[j] = __fmul2_rn(__fmul2_rn(h[i].p[j], rho2), w.p[j]);
+        if (p.y && in[i]) store_pairs<false>(p.y, row + v, h[i]);
         if (p.codes) {
           const int b = v >> 2;
-          const int64_t s = p.atoms ? sf_atom_word(t >> 7, b >> 2, p.d / 128, (int)(t & 127)) + (b & 3) : t * (nvec >> 2) + b;
-          quantise8(h[i], in[i], p.codes, t * nvec + v, p.scales + s, (v & 3) == 0);
+          const int64_t s = p.atoms ? sf_atom_word(t >> 7, b >> 2, p.d / 128, t & 127) + (b & 3) : (row + v) >> 2;
+          quantise8(h[i], in[i], p.codes, row + v, p.scales + s, (v & 3) == 0);
         }
       }
     }
     gate = next_gate;
-    last = at;
-    at = next;
+    t += step;
+    row += row_step;
+    q.next();
   }
-  for (; t < p.rows; t += step)  // padding rows of the scale atoms
+  for (int64_t r = t; r < p.rows; r += step)  // padding rows of the scale atoms
     for (int kb = threadIdx.x; kb < p.d / 128; kb += blockDim.x)
-      *reinterpret_cast<uint32_t*>(p.scales + sf_atom_word(t >> 7, kb, p.d / 128, (int)(t & 127))) = 0;
+      *reinterpret_cast<uint32_t*>(p.scales + sf_atom_word(r >> 7, kb, p.d / 128, (int)(r & 127))) = 0;
 }
 
 struct SandwichBwdParams {
@@ -230,23 +285,52 @@ struct SandwichBwdParams {
   int post_f32, gate_f32, weight_f32, depth;
 };
 
-// PACKED: x and h come as codes and scales.
+// A vector of x or h as it is kept between the phases of a row: bf16 as it came, or E4M3 codes as f16
+// pairs (which hold them exactly) and their block's scale.
+template <bool PACKED>
+struct Held {
+  uint4 u;
+  float s;
+  __device__ __forceinline__ Pairs value() const {  // without the scale
+    if constexpr (!PACKED) return pairs(unpack8(u));
+    Pairs r;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.p[j] = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+    return r;
+  }
+  __device__ __forceinline__ float scale() const { return PACKED ? s : 1.0f; }
+};
+
+// PACKED: x and h come as codes and scales.  Three phases per row: the sums that give rho1, rho2 and the
+// mean over g hhat; ds with everything summed over rows, and q; dx.  The first runs a row ahead beside
+// the second, so that one exchange serves both.  A place of the ring is free after that exchange (x
+// waits for the third phase in registers).
 template <int V, bool F32, bool PACKED, bool RING, int MT>
 __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p) {
-  __shared__ float smem[2][32][4];
+  __shared__ float smem[2][4][16];
+  __shared__ __align__(8) uint64_t bars[3];
+  __shared__ int s_abort;
   extern __shared__ __align__(16) uint8_t ring[];
-  const int nvec = p.d >> 3;
-  const int64_t row_step = (int64_t)gridDim.x * nvec;  // vectors from a turn's row to the next one's
-  const int64_t end = p.T * nvec;
-  constexpr bool kHold = V <= 2;
+  const int nvec = p.d >> 3, T = (int)p.T;
+  int t = blockIdx.x;  // gridDim.x <= T
+  int64_t row = (int64_t)t * nvec;  // vectors before the row
+  const int64_t row_step = (int64_t)gridDim.x * nvec;
+  constexpr bool kHold = V <= 2;    // W in registers; else the weights are read where they are used
+  constexpr bool kShared = V == 2;  // the next norm's weight in shared memory behind the ring, in fp32
+  constexpr bool kPlainH = F32 && !PACKED;  // h is fp32
   const bool next_norm = p.dy != nullptr, has_res = p.dres != nullptr;
-  // planes of a place: dy, dres, h, x; codes with a word of scales (the vector's is one of its four bytes)
-  constexpr int kRes = F32 ? 32 : 16, kH = PACKED ? 12 : kRes, kX = PACKED ? 12 : 16;
+  // planes of a place: dy, dres, h, x, and for codes the two tensors' scales
+  constexpr int kRes = F32 ? 32 : 16, kH = PACKED ? 8 : kRes, kX = PACKED ? 8 : 16;
+  const uint32_t scale_bytes = PACKED ? (nvec / 4 + 31) & ~15 : 0;
   const uint32_t res_at = next_norm ? 16 * nvec : 0, h_at = res_at + (has_res ? kRes * nvec : 0);
-  const uint32_t x_at = h_at + (next_norm ? kH * nvec : 0), place = (x_at + kX * nvec + 15) & ~15u;
-  const uint32_t base = smem_u32(ring);
+  const uint32_t x_at = h_at + (next_norm ? kH * nvec : 0), xs_at = x_at + kX * nvec, hs_at = xs_at + scale_bytes;
+  RowRing q{smem_u32(ring), hs_at + (next_norm ? scale_bytes : 0), smem_u32(bars), p.depth, 0, 0, true};
+  const uint32_t w_at = q.base + p.depth * q.place;
+  const int64_t scale_end = PACKED ? ((p.T * nvec) >> 2) & ~(int64_t)15 : 0;  // whole 16 bytes of scales
   bool in[V];
-  Pairs A[V], dw[V], W[kHold ? V : 1], w2[kHold ? V : 1];
+  Pairs A[V], dw[V], W[kHold ? V : 1], w2[1];
+  Held<PACKED> x_row[V], x_next[V], h_next[V];
   auto inner = [&](int v, bool ok) {
     Vec8 a = load_weight(p.post, p.post_f32, v, ok);
     if (p.gate) {
@@ -257,174 +341,211 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
     return pairs(a);
   };
   auto weight_of = [&](int i) {
-    return kHold ? w2[kHold ? i : 0] : pairs(load_weight(p.weight, p.weight_f32, threadIdx.x + i * blockDim.x, true));
+    const int v = threadIdx.x + i * blockDim.x;
+    if constexpr (V == 1) return w2[0];
+    else if constexpr (kShared) return pairs(value8<true>(ring8<true>(w_at, v, nvec)));
+    else return pairs(load_weight(p.weight, p.weight_f32, v, true));
   };
   auto inner_of = [&](int i) { return kHold ? W[kHold ? i : 0] : inner(threadIdx.x + i * blockDim.x, true); };
-  auto copy_packed = [&](uint32_t at, const void* codes, const uint8_t* scales, int64_t row, int v) {
-    if (v >= nvec) return;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at + 8 * v), "l"(static_cast<const uint2*>(codes) + row + v) : "memory");
-    // a row has nvec / 4 scales; nvec is a multiple of 16, so the four around the vector's are a word
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 8 * nvec + 4 * v), "l"(scales + (row >> 2) + (v >> 4) * 4) : "memory");
-  };
-  auto fetch = [&](int64_t row, uint32_t at) {
-    if constexpr (!RING) return;
-    if (row < end) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (next_norm) copy8<false>(at, p.dy, row, v, nvec);
-        if (has_res) copy8<F32>(at + res_at, p.dres, row, v, nvec);
-        if constexpr (PACKED) {
-          if (next_norm) copy_packed(at + h_at, p.h, p.h_scales, row, v);
-          copy_packed(at + x_at, p.x, p.x_scales, row, v);
-        } else {
-          if (next_norm) copy8<F32>(at + h_at, p.h, row, v, nvec);
-          copy8<false>(at + x_at, p.x, row, v, nvec);
-        }
-      }
+  // The row `ahead` of the present one; every read of what is in its place has ended.  A row's scales need
+  // not be whole 16 bytes: those around them are copied, up to the last whole ones of the tensor.
+  auto fetch = [&](int ahead) {
+    if (RING && threadIdx.x == 0 && t + (int64_t)ahead * gridDim.x < T) {
+      const int64_t from = row + ahead * row_step;
+      const uint32_t at = ahead == q.depth ? q.at(0) : q.at(ahead), bar = ahead == q.depth ? q.bar(0) : q.bar(ahead);
+      const int64_t s0 = (from >> 2) & ~(int64_t)15, s1 = min((((from + nvec) >> 2) + 15) & ~(int64_t)15, scale_end);
+      const uint32_t scales = PACKED && s1 > s0 ? (uint32_t)(s1 - s0) : 0;
+      mbar_arrive_expect_tx(bar, xs_at + (next_norm ? 2 : 1) * scales);
+      if (next_norm) bulk_load(at, static_cast<const uint4*>(p.dy) + from, 16 * nvec, bar);
+      if (has_res) bulk_load(at + res_at, static_cast<const char*>(p.dres) + kRes * from, kRes * nvec, bar);
+      if (next_norm) bulk_load(at + h_at, static_cast<const char*>(p.h) + kH * from, kH * nvec, bar);
+      bulk_load(at + x_at, static_cast<const char*>(p.x) + kX * from, kX * nvec, bar);
+      if (scales) bulk_load(at + xs_at, p.x_scales + s0, scales, bar);
+      if (scales && next_norm) bulk_load(at + hs_at, p.h_scales + s0, scales, bar);
     }
-    copies_end();
   };
-  auto unpacked = [&](uint32_t at, const void* codes, const uint8_t* scales, int64_t row, int v) {
-    uint2 q;
-    uint32_t s;
-    if constexpr (RING) {
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "r"(at + 8 * v));
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(s) : "r"(at + 8 * nvec + 4 * v));
-      s = (s >> (2 * (v & 12))) & 255u;
+  auto read_dy = [&](int64_t from, int ahead, int v) {
+    if constexpr (RING) return row_pairs<false>(q.at(ahead), v);
+    else return pairs(load8<false>(p.dy, from + v));
+  };
+  auto held = [&](int64_t from, int ahead, uint32_t plane, uint32_t scale_plane, const void* rows, const uint8_t* scales, int v) {
+    Held<PACKED> r{};
+    if constexpr (!PACKED) {
+      if constexpr (RING) r.u = ring16(q.at(ahead) + plane + 16 * v);
+      else r.u = static_cast<const uint4*>(rows)[from + v];
     } else {
-      q = static_cast<const uint2*>(codes)[row + v];
-      s = scales[(row + v) >> 2];
+      uint2 c;
+      uint32_t byte;
+      if constexpr (RING) {
+        const int64_t s = from >> 2;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(q.at(ahead) + plane + 8 * v));
+        if (s + (nvec >> 2) <= scale_end || s + (v >> 2) < scale_end)
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(q.at(ahead) + scale_plane + ((uint32_t)s & 15) + (v >> 2)));
+        else
+          byte = scales[s + (v >> 2)];
+      } else {
+        c = static_cast<const uint2*>(rows)[from + v];
+        byte = scales[(from + v) >> 2];
+      }
+      r.u = e4m3_halves(c);
+      r.s = mx_scale(byte);
     }
-    return dequantise8(q, mx_scale(s));
+    return r;
   };
-  auto read_dy = [&](int64_t row, uint32_t at, int v) {
-    if constexpr (RING) return pairs(value8<false>(ring8<false>(at, v, nvec)));
-    else return pairs(load8<false>(p.dy, row + v));
+  auto read_plain_h = [&](int64_t from, int ahead, int v) {
+    if constexpr (RING) return row_pairs<true>(q.at(ahead) + h_at, v);
+    else return pairs(load8<true>(p.h, from + v));
   };
-  auto read_res = [&](int64_t row, uint32_t at, int v) {
-    if constexpr (RING) return pairs(value8<F32>(ring8<F32>(at + res_at, v, nvec)));
-    else return pairs(load8<F32>(p.dres, row + v));
-  };
-  auto read_h = [&](int64_t row, uint32_t at, int v) {
-    if constexpr (PACKED) return pairs(unpacked(at + h_at, p.h, p.h_scales, row, v));
-    else if constexpr (RING) return pairs(value8<F32>(ring8<F32>(at + h_at, v, nvec)));
-    else return pairs(load8<F32>(p.h, row + v));
-  };
-  auto read_x = [&](int64_t row, uint32_t at, int v) {
-    if constexpr (PACKED) return pairs(unpacked(at + x_at, p.x, p.x_scales, row, v));
-    else if constexpr (RING) return pairs(value8<false>(ring8<false>(at + x_at, v, nvec)));
-    else return pairs(load8<false>(p.x, row + v));
-  };
-  // this thread's share of a row's sum h^2, sum dy weight h, sum x^2
-  auto sums_of = [&](int64_t row, uint32_t at, float& hh, float& dot, float& xx) {
-    float2 a = both(0.0f), b = both(0.0f), c = both(0.0f);
+  // this thread's share of a row's sum h^2, sum dy weight h, sum x^2; keeps x and h for the next phases
+  auto sums_of = [&](int64_t from, int ahead, float& hh, float& dot, float& xx) {
+    hh = dot = xx = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (in[i]) {
         const int v = threadIdx.x + i * blockDim.x;
-        const Pairs x = read_x(row, at, v);
+        x_next[i] = held(from, ahead, x_at, xs_at, p.x, p.x_scales, v);
+        const Pairs x = x_next[i].value();
+        float2 c = both(0.0f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) c = __ffma2_rn(x.p[j], x.p[j], c);
+        xx = fmaf(c.x + c.y, x_next[i].scale() * x_next[i].scale(), xx);
         if (next_norm) {
-          const Pairs h = read_h(row, at, v), dy = read_dy(row, at, v), w = weight_of(i);
+          Pairs h;
+          float s = 1.0f;
+          if constexpr (kPlainH) {
+            h = read_plain_h(from, ahead, v);
+          } else {
+            h_next[i] = held(from, ahead, h_at, hs_at, p.h, p.h_scales, v);
+            h = h_next[i].value();
+            s = h_next[i].scale();
+          }
+          const Pairs dy = read_dy(from, ahead, v), w = weight_of(i);
+          float2 a = both(0.0f), b = both(0.0f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             a = __ffma2_rn(h.p[j], h.p[j], a);
             b = __ffma2_rn(h.p[j], __fmul2_rn(dy.p[j], w.p[j]), b);
           }
+          hh = fmaf(a.x + a.y, s * s, hh);
+          dot = fmaf(b.x + b.y, s, dot);
         }
       }
     }
-    hh = a.x + a.y;
-    dot = b.x + b.y;
-    xx = c.x + c.y;
+    if (!q.ok) xx = NAN;
   };
-  int64_t row = (int64_t)blockIdx.x * nvec;  // gridDim.x <= T
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    in[i] = threadIdx.x + i * blockDim.x < nvec;
+    in[i] = i < V - 1 || threadIdx.x + i * blockDim.x < nvec;  // only the last can be past the row
+    x_row[i] = x_next[i] = h_next[i] = Held<PACKED>{};
 #pragma unroll
     for (int j = 0; j < 4; ++j) A[i].p[j] = dw[i].p[j] = both(0.0f);
   }
-  uint32_t at = base, last = base + (p.depth - 1) * place;  // this row's place; the one before it
-  fetch(row, base);
-  fetch(row + row_step, base + place);
+  if (RING && threadIdx.x == 0) {
+    for (int k = 0; k < p.depth; ++k) mbar_init(q.bars + 8 * k, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  for (int i = threadIdx.x; i < 128; i += blockDim.x) (&smem[0][0][0])[i] = 0.0f;
+  __syncthreads();
+  for (int k = 0; k < p.depth; ++k) fetch(k);
 #pragma unroll
   for (int i = 0; i < (kHold ? V : 0); ++i) {
-    W[i] = inner(threadIdx.x + i * blockDim.x, in[i]);
-    w2[i] = pairs(next_norm ? load_weight(p.weight, p.weight_f32, threadIdx.x + i * blockDim.x, in[i]) : Vec8{});
+    const int v = threadIdx.x + i * blockDim.x;
+    W[i] = inner(v, in[i]);
+    const Vec8 w = next_norm ? load_weight(p.weight, p.weight_f32, v, in[i]) : Vec8{};
+    if constexpr (V == 1) {
+      w2[0] = pairs(w);
+    } else if (in[i]) {  // read back by this thread alone
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(w_at + 16 * v), "f"(w.v[0]), "f"(w.v[1]), "f"(w.v[2]), "f"(w.v[3]) : "memory");
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(w_at + 16 * (nvec + v)), "f"(w.v[4]), "f"(w.v[5]), "f"(w.v[6]), "f"(w.v[7]) : "memory");
+    }
   }
-  if constexpr (RING) copies_wait<1>();
-  int64_t t = blockIdx.x;
   float gate = p.token_gate ? p.token_gate[t] : 1.0f, next_gate = 1.0f;
   float sums[4];  // h^2, dy weight h, x^2 of the next row; ds W x of this one
-  sums_of(row, base, sums[0], sums[1], sums[2]);
+  if constexpr (RING) q.wait(0, &s_abort);
+  sums_of(row, 0, sums[0], sums[1], sums[2]);
   sums[3] = 0.0f;
   row_sums(sums, smem, 1);
-  for (int turn = 0; row < end; row += row_step, t += gridDim.x, turn ^= 1) {
-    fetch(row + 2 * row_step, last);
-    if constexpr (RING) copies_wait<1>();
-    const uint32_t next = at + place == base + p.depth * place ? base : at + place;
-    if (p.token_gate && row + row_step < end) next_gate = p.token_gate[t + gridDim.x];
+  const float2 a2 = both(p.res_scale);
+  for (int turn = 0; t < T; turn ^= 1) {
+    const bool more = t + (int)gridDim.x < T;
+    if (p.token_gate && more) next_gate = p.token_gate[t + gridDim.x];
     const float rho1 = rsqrtf(fmaf(sums[2], p.inv_d, p.eps)), rho2 = rsqrtf(fmaf(sums[0], p.inv_d, p.eps));
-    const float2 r2 = both(rho2), c2 = both(-sums[1] * p.inv_d * rho2 * rho2);  // - mean(g hhat) rho2
-    const float2 rt = both(rho1 * gate), a2 = both(p.res_scale);
+    const float c2 = -sums[1] * p.inv_d * rho2 * rho2, rt = rho1 * gate;  // - mean(g hhat) rho2
+    const float2 r2 = both(rho2);
     Pairs ds[V];
-    float2 q = both(0.0f);
+    float qx = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (in[i]) {
-        if (has_res) ds[i] = read_res(row, at, v);
-        else ds[i] = pairs(Vec8{});
+        ds[i] = Pairs{};
+        if (has_res) {
+          if constexpr (RING) ds[i] = row_pairs<F32>(q.at(0) + res_at, v);
+          else ds[i] = pairs(load8<F32>(p.dres, row + v));
+        }
         if (next_norm) {
-          const Pairs h = read_h(row, at, v), dy = read_dy(row, at, v), w = weight_of(i);
+          Pairs h;
+          float s = 1.0f;
+          if constexpr (kPlainH) {
+            h = read_plain_h(row, 0, v);
+          } else {
+            h = h_next[i].value();
+            s = h_next[i].scale();
+          }
+          const Pairs dy = read_dy(row, 0, v), w = weight_of(i);
+          const float2 rs = both(rho2 * s), cs = both(c2 * s);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            dw[i].p[j] = __ffma2_rn(dy.p[j], __fmul2_rn(h.p[j], r2), dw[i].p[j]);
-            const float2 g = __ffma2_rn(h.p[j], c2, __fmul2_rn(dy.p[j], w.p[j]));
+            dw[i].p[j] = __ffma2_rn(dy.p[j], __fmul2_rn(h.p[j], rs), dw[i].p[j]);
+            const float2 g = __ffma2_rn(h.p[j], cs, __fmul2_rn(dy.p[j], w.p[j]));
             ds[i].p[j] = __ffma2_rn(g, r2, ds[i].p[j]);
           }
         }
-        const Pairs x = read_x(row, at, v), w = inner_of(i);
-        Vec8 o;
+        x_row[i] = x_next[i];
+        const Pairs x = x_row[i].value(), w = inner_of(i);
+        const float2 rs = both(rt * x_row[i].scale());
+        float2 qs = both(0.0f);
+        Pairs o;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 dx = __fmul2_rn(ds[i].p[j], x.p[j]);
-          A[i].p[j] = __ffma2_rn(dx, rt, A[i].p[j]);
-          q = __ffma2_rn(dx, w.p[j], q);
-          const float2 r = __fmul2_rn(ds[i].p[j], a2);
-          o.v[2 * j] = r.x;
-          o.v[2 * j + 1] = r.y;
+          A[i].p[j] = __ffma2_rn(dx, rs, A[i].p[j]);
+          qs = __ffma2_rn(dx, w.p[j], qs);
+          o.p[j] = __fmul2_rn(ds[i].p[j], a2);
         }
-        store8<F32>(p.dresidual, row + v, o);
+        qx = fmaf(qs.x + qs.y, x_row[i].scale(), qx);
+        store_pairs<F32>(p.dresidual, row + v, o);
       }
     }
     sums[0] = sums[1] = sums[2] = 0.0f;
-    if (row + row_step < end) sums_of(row + row_step, next, sums[0], sums[1], sums[2]);
-    sums[3] = q.x + q.y;
+    if (more) {
+      if constexpr (RING) q.wait(1, &s_abort);
+      sums_of(row + row_step, 1, sums[0], sums[1], sums[2]);
+    }
+    sums[3] = qx;
     row_sums(sums, smem, turn);
-    const float2 c1 = both(-sums[3] * p.inv_d * rho1 * rho1);  // - mean(ds W xhat) rho1
+    if (blockDim.x == 32) __syncwarp();
+    fetch(q.depth);  // into this row's place
+    const float c1 = -sums[3] * p.inv_d * rho1 * rho1;  // - mean(ds W xhat) rho1
+    const float2 rt2 = both(rt);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (in[i]) {
-        const Pairs x = read_x(row, at, v), w = inner_of(i);
-        Vec8 o;
+        const Pairs x = x_row[i].value(), w = inner_of(i);
+        const float2 cs = both(c1 * x_row[i].scale());
+        Pairs o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 r = __fmul2_rn(__ffma2_rn(x.p[j], c1, __fmul2_rn(ds[i].p[j], w.p[j])), rt);
-          o.v[2 * j] = r.x;
-          o.v[2 * j + 1] = r.y;
-        }
-        store8<false>(p.dx, row + v, o);
+        for (int j = 0; j < 4; ++j) o.p[j] = __fmul2_rn(__ffma2_rn(x.p[j], cs, __fmul2_rn(ds[i].p[j], w.p[j])), rt2);
+        store_pairs<false>(p.dx, row + v, o);
       }
     }
     if (p.dtoken_gate && threadIdx.x == 0) p.dtoken_gate[t] = rho1 * sums[3];
     gate = next_gate;
-    last = at;
-    at = next;
+    t += gridDim.x;
+    row += row_step;
+    q.next();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   float* mine = p.partial + (int64_t)blockIdx.x * p.d;
@@ -432,16 +553,8 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
   for (int i = 0; i < V; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (in[i]) {
-      Vec8 a, b;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a.v[2 * j] = A[i].p[j].x;
-        a.v[2 * j + 1] = A[i].p[j].y;
-        b.v[2 * j] = dw[i].p[j].x;
-        b.v[2 * j + 1] = dw[i].p[j].y;
-      }
-      store8<true>(mine, v, a);
-      if (next_norm) store8<true>(mine + (int64_t)gridDim.x * p.d, v, b);
+      store_pairs<true>(mine, v, A[i]);
+      if (next_norm) store_pairs<true>(mine + (int64_t)gridDim.x * p.d, v, dw[i]);
     }
   }
 }
@@ -535,12 +648,14 @@ constexpr int kThreadsPerSm = 512;  // 128 registers each
 static int sandwich_bwd_grid(int sms, int64_t T, int d) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(T, (int64_t)sms * sandwich_shape(d, false, kThreadsPerSm).blocks));
 }
-// Places of the ring for the rows that a block has to take, at most three; 0 where they do not fit and
-// for the widest rows (rows are then read from memory, the second time from L2).
-static int ring_depth(int64_t turns, int blocks, int64_t bytes, int v) {
+// Places of the ring for the rows that a block has to take, three or two; 0 where they do not fit beside
+// `more` bytes, and for the widest rows (they are then read from memory, the second time from L2).
+static int ring_depth(int64_t turns, int blocks, int64_t bytes, int64_t more, int v) {
   if (v > 4) return 0;
-  const int depth = (int)std::min<int64_t>(3, turns);
-  return depth * bytes <= kSmemPerSm / blocks - kSmemOwn ? depth : 0;
+  const int64_t room = kSmemPerSm / blocks - kSmemOwn - more;
+  for (int depth = 3; depth >= 2; --depth)
+    if (std::min<int64_t>(depth, turns) * bytes <= room) return (int)std::min<int64_t>(depth, turns);
+  return 0;
 }
 template <class K>
 static cudaError_t allow_smem(K k, int64_t smem) {
@@ -586,7 +701,7 @@ int mok_sandwich_norm(const mok_sandwich* a, int64_t T, int d, const void* x, co
   const int64_t row_bytes = 2 * d * (f32 ? 3 : 2);
   const int64_t groups = (p.rows + n.rows - 1) / n.rows, most = (int64_t)sms * n.blocks;
   const int grid = (int)std::min<int64_t>(groups, most);
-  p.depth = ring_depth((T + (int64_t)grid * n.rows - 1) / ((int64_t)grid * n.rows), n.blocks, n.rows * row_bytes, n.v);
+  p.depth = ring_depth((T + (int64_t)grid * n.rows - 1) / ((int64_t)grid * n.rows), n.blocks, n.rows * row_bytes, 0, n.v);
   const int64_t smem = p.depth * n.rows * row_bytes;
   void (*k)(const SandwichParams) = nullptr;
   auto pick = [&](auto type, auto ring) {
@@ -654,9 +769,11 @@ int mok_sandwich_norm_backward(const mok_sandwich* a, int64_t T, int d, const vo
                       a->weight_type == MOK_T_F32, 0};
   const SandwichShape n = sandwich_shape(d, false, kThreadsPerSm);
   const int64_t nvec = d / 8, res = f32 ? 32 : 16;
-  const int64_t row_bytes = (nvec * ((dy ? 16 : 0) + (dres ? res : 0) + (dy ? (packed ? 12 : res) : 0) + (packed ? 12 : 16)) + 15) / 16 * 16;
-  p.depth = ring_depth((T + grid - 1) / grid, n.blocks, row_bytes, n.v);
-  const int64_t smem = p.depth * row_bytes;
+  const int64_t scales = packed ? (nvec / 4 + 31) / 16 * 16 : 0;  // as the kernel lays a place out
+  const int64_t row_bytes = nvec * ((dy ? 16 : 0) + (dres ? res : 0) + (dy ? (packed ? 8 : res) : 0) + (packed ? 8 : 16)) + scales * (dy ? 2 : 1);
+  const int64_t own = n.v == 2 ? 4 * d : 0;  // the next norm's weight
+  p.depth = ring_depth((T + grid - 1) / grid, n.blocks, row_bytes, own, n.v);
+  const int64_t smem = p.depth * row_bytes + own;
   void (*k)(const SandwichBwdParams) = nullptr;
   auto pick = [&](auto type, auto codes, auto ring) {
     constexpr bool F = decltype(type)::value, C = decltype(codes)::value, R = decltype(ring)::value;
