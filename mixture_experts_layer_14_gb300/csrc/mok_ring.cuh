@@ -72,11 +72,8 @@ __device__ __forceinline__ Vec8 load_weight(const void* w, int f32, int v, bool 
   return f32 ? load8<true>(w, v) : load8<false>(w, v);
 }
 
-// Values of eight E4M3 codes times their block's scale (a UE8M0 byte; every product is exact but
-// where it leaves fp32's range).
-__device__ __forceinline__ float mx_scale(uint32_t byte) {
-  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
-}
+// 2^(byte - 127): a UE8M0 scale (255, which no block has, gives infinity).
+__device__ __forceinline__ float mx_scale(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
 __device__ __forceinline__ uint4 e4m3_halves(uint2 q) {  // as f16, which holds every E4M3 value
   uint4 r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.x) : "h"((uint16_t)q.x));
@@ -85,6 +82,8 @@ __device__ __forceinline__ uint4 e4m3_halves(uint2 q) {  // as f16, which holds 
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.w) : "h"((uint16_t)(q.y >> 16)));
   return r;
 }
+// Values of eight E4M3 codes times their block's scale (every product is exact but where it leaves
+// fp32's range).
 __device__ __forceinline__ Vec8 dequantise8(uint2 q, float scale) {
   Vec8 r;
   const uint4 u = e4m3_halves(q);

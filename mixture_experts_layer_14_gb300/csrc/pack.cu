@@ -6,6 +6,7 @@
 // or 8 lanes hold a block), which keeps every access of a warp contiguous, and has several vectors
 // under way.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "mok_ring.cuh"
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kPackThreads) unpack_kernel(const __grid_const
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int64_t v = first + i * kPackThreads;
-    const Vec8 w = dequantise8(q[i], mx_scale(byte[i]));
+    const Vec8 w = dequantise8(q[i], byte[i] == 255 ? NAN : mx_scale(byte[i]));
     uint4 o = pack8(w);
     if constexpr (F32) o = make_uint4(__float_as_uint(w.v[0]), __float_as_uint(w.v[1]), __float_as_uint(w.v[2]), __float_as_uint(w.v[3]));
     if (v < n) static_cast<uint4*>(p.wide_out[s])[v] = o;

@@ -42,39 +42,28 @@ struct SandwichParams {
   int post_f32, gate_f32, weight_f32, atoms, depth;
 };
 
-// Sums of N = 2 or 4 values over the row's threads, the same in all of them: a row is a block's, of at most
-// 16 warps, or a warp's (32 threads in x).  While values are left a step of the tree halves their number
-// instead of adding all of them up in every lane, which takes a third of the instructions.  `turn`
-// alternates between calls: two buffers need one barrier per call.  smem is zero where there is no warp.
-template <int N>
-__device__ __forceinline__ void row_sums(float (&a)[N], float (&smem)[2][N][16], int turn) {
+// Sums of two values over the row's threads, the same in all of them: a row is a block's, of at most 16
+// warps, or a warp's (32 threads in x).  The first step of the tree leaves each half of a warp with one of
+// the values.  `turn` alternates between calls: two buffers need one barrier per call.  smem is zero
+// where there is no warp.
+__device__ __forceinline__ void row_sums(float (&a)[2], float (&smem)[2][2][16], int turn) {
   constexpr unsigned kFull = 0xffffffffu;
-  constexpr int L = 32 / N;  // lanes that share a value in the end
-  const int lane = threadIdx.x & 31, value = lane / L;
-  float v;
-  if constexpr (N == 4) {
-    const bool hi = lane & 16;
-    const float x = (hi ? a[2] : a[0]) + __shfl_xor_sync(kFull, hi ? a[0] : a[2], 16);
-    const float y = (hi ? a[3] : a[1]) + __shfl_xor_sync(kFull, hi ? a[1] : a[3], 16);
-    const bool up = lane & 8;
-    v = (up ? y : x) + __shfl_xor_sync(kFull, up ? x : y, 8);
-  } else {
-    const bool hi = lane & 16;
-    v = (hi ? a[1] : a[0]) + __shfl_xor_sync(kFull, hi ? a[0] : a[1], 16);
-  }
+  const int lane = threadIdx.x & 31;
+  const bool hi = lane & 16;
+  float v = (hi ? a[1] : a[0]) + __shfl_xor_sync(kFull, hi ? a[0] : a[1], 16);
 #pragma unroll
-  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   if (blockDim.x > 32) {
-    if (lane % L == 0) smem[turn][value][threadIdx.x >> 5] = v;
+    if ((lane & 15) == 0) smem[turn][hi][threadIdx.x >> 5] = v;
     __syncthreads();
-    v = smem[turn][value][lane % L];
-    if constexpr (N == 4) v += smem[turn][value][lane % L + 8];
+    v = smem[turn][hi][lane & 15];
 #pragma unroll
-    for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) a[i] = __shfl_sync(kFull, v, i * L);
+  a[0] = __shfl_sync(kFull, v, 0);
+  a[1] = __shfl_sync(kFull, v, 16);
 }
+
 // MXFP8 form of eight elements whose block of 32 lies in four neighbouring lanes.
 __device__ __forceinline__ void quantise8(const Pairs& a, bool in, void* codes, int64_t at, uint8_t* scale, bool first) {
   float amax = 0.0f;
@@ -285,52 +274,114 @@ struct SandwichBwdParams {
   int post_f32, gate_f32, weight_f32, depth;
 };
 
-// A vector of x or h as it is kept between the phases of a row: bf16 as it came, or E4M3 codes as f16
-// pairs (which hold them exactly) and their block's scale.
-template <bool PACKED>
-struct Held {
-  uint4 u;
-  float s;
-  __device__ __forceinline__ Pairs value() const {  // without the scale
-    if constexpr (!PACKED) return pairs(unpack8(u));
-    Pairs r;
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Six sums of a row (an array of eight, two of them empty) over the consumer warps.  In put_sums every step
+// of the tree halves the number of values that a lane still has; the four lanes of value i then hold its
+// sum over the warp.  get_sums joins up to 16 warps.  smem is zero where there is no warp.
+__device__ __forceinline__ void put_sums(const float (&a)[8], float (&smem)[8][16], int warp) {
+  constexpr unsigned kFull = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  float b[4], c[2];
+  const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.p[j] = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-    return r;
-  }
-  __device__ __forceinline__ float scale() const { return PACKED ? s : 1.0f; }
-};
+  for (int i = 0; i < 4; ++i) b[i] = (h16 ? a[i + 4] : a[i]) + __shfl_xor_sync(kFull, h16 ? a[i] : a[i + 4], 16);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) c[i] = (h8 ? b[i + 2] : b[i]) + __shfl_xor_sync(kFull, h8 ? b[i] : b[i + 2], 8);
+  float v = (h4 ? c[1] : c[0]) + __shfl_xor_sync(kFull, h4 ? c[0] : c[1], 4);
+  v += __shfl_xor_sync(kFull, v, 2);
+  v += __shfl_xor_sync(kFull, v, 1);
+  if ((lane & 3) == 0) smem[lane >> 2][warp] = v;
+}
+__device__ __forceinline__ void get_sums(float (&a)[6], float (&smem)[8][16]) {
+  constexpr unsigned kFull = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const float4 q = reinterpret_cast<const float4*>(smem[lane >> 2])[lane & 3];
+  float v = (q.x + q.y) + (q.z + q.w);
+  v += __shfl_xor_sync(kFull, v, 2);
+  v += __shfl_xor_sync(kFull, v, 1);
+#pragma unroll
+  for (int i = 0; i < 6; ++i) a[i] = __shfl_sync(kFull, v, 4 * i);
+}
 
-// PACKED: x and h come as codes and scales.  Three phases per row: the sums that give rho1, rho2 and the
-// mean over g hhat; ds with everything summed over rows, and q; dx.  The first runs a row ahead beside
-// the second, so that one exchange serves both.  A place of the ring is free after that exchange (x
-// waits for the third phase in registers).
+// PACKED: x and h come as codes and scales.  The mean over ds W xhat, which dx needs, would follow from
+// ds and so from the means before it; written out,
+//   sum ds W x = rho2 (sum g W x + c2 sum h W x) + sum dres W x,  c2 = - rho2^2 mean(g h),
+// it takes sums of the inputs alone, so that one pass over a row gives all six sums and one exchange
+// serves it; a second pass gives ds, dx and what is summed over rows.  The first pass runs a row ahead:
+// its exchange (an mbarrier that the warps arrive on) ends under the second pass of the row before.
+// One more warp fetches rows as their places come free.
+// Rows of fp32 without codes, of which only two may fit, take the second pass first, so that the next
+// fetch has the first pass and the exchange to land.
 template <int V, bool F32, bool PACKED, bool RING, int MT>
 __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p) {
-  __shared__ float smem[2][4][16];
-  __shared__ __align__(8) uint64_t bars[3];
+  __shared__ __align__(16) float smem[2][8][16];
+  __shared__ __align__(8) uint64_t s_bars[7];  // full and empty, three each; the exchange
   __shared__ int s_abort;
   extern __shared__ __align__(16) uint8_t ring[];
   const int nvec = p.d >> 3, T = (int)p.T;
+  const int threads = RING ? blockDim.x - 32 : blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int t = blockIdx.x;  // gridDim.x <= T
   int64_t row = (int64_t)t * nvec;  // vectors before the row
   const int64_t row_step = (int64_t)gridDim.x * nvec;
-  constexpr bool kHold = V <= 2;    // W in registers; else the weights are read where they are used
-  constexpr bool kShared = V == 2;  // the next norm's weight in shared memory behind the ring, in fp32
-  constexpr bool kPlainH = F32 && !PACKED;  // h is fp32
+  constexpr bool kHold = V <= 2;  // the weights in registers; else they are read where they are used
+  constexpr bool kLate = F32 && !PACKED;
   const bool next_norm = p.dy != nullptr, has_res = p.dres != nullptr;
   // planes of a place: dy, dres, h, x, and for codes the two tensors' scales
   constexpr int kRes = F32 ? 32 : 16, kH = PACKED ? 8 : kRes, kX = PACKED ? 8 : 16;
   const uint32_t scale_bytes = PACKED ? (nvec / 4 + 31) & ~15 : 0;
   const uint32_t res_at = next_norm ? 16 * nvec : 0, h_at = res_at + (has_res ? kRes * nvec : 0);
   const uint32_t x_at = h_at + (next_norm ? kH * nvec : 0), xs_at = x_at + kX * nvec, hs_at = xs_at + scale_bytes;
-  RowRing q{smem_u32(ring), hs_at + (next_norm ? scale_bytes : 0), smem_u32(bars), p.depth, 0, 0, true};
-  const uint32_t w_at = q.base + p.depth * q.place;
-  const int64_t scale_end = PACKED ? ((p.T * nvec) >> 2) & ~(int64_t)15 : 0;  // whole 16 bytes of scales
+  const uint32_t place = hs_at + (next_norm ? scale_bytes : 0), base = smem_u32(ring);
+  const uint32_t full = smem_u32(s_bars), empty = full + 24, exchange = full + 48;
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 3; ++k) {
+      mbar_init(full + 8 * k, 1);
+      mbar_init(empty + 8 * k, threads >> 5);
+    }
+    mbar_init(exchange, threads >> 5);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  for (int i = threadIdx.x; i < 256; i += blockDim.x) (&smem[0][0][0])[i] = 0.0f;
+  __syncthreads();
+
+  if (RING && (int)threadIdx.x >= threads) {
+    // The producer.  A row's scales need not be whole 16 bytes: those around them are copied, up to the
+    // last whole ones of the tensor; what is left at its end is stored before the arrival that others
+    // wait for.
+    const int64_t scale_end = PACKED ? ((p.T * nvec) >> 2) & ~(int64_t)15 : 0;
+    if (lane == 0) {
+      int k = 0;
+      uint32_t phase = 1;  // a place's first wait ends at once
+      for (; t < T; t += gridDim.x, row += row_step) {
+        if (!mbar_wait(empty + 8 * k, phase, nullptr, &s_abort)) break;
+        const uint32_t at = base + k * place, bar = full + 8 * k;
+        const int64_t s0 = (row >> 2) & ~(int64_t)15, s1 = min((((row + nvec) >> 2) + 15) & ~(int64_t)15, scale_end);
+        const uint32_t scales = PACKED && s1 > s0 ? (uint32_t)(s1 - s0) : 0;
+        if constexpr (PACKED) {
+          for (int64_t b = max(s0, scale_end); b < (row + nvec) >> 2; ++b) {
+            const uint32_t to = at + (uint32_t)(b - s0);
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + xs_at), "r"((uint32_t)p.x_scales[b]) : "memory");
+            if (next_norm) asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + hs_at), "r"((uint32_t)p.h_scales[b]) : "memory");
+          }
+        }
+        mbar_arrive_expect_tx(bar, xs_at + (next_norm ? 2 : 1) * scales);
+        if (next_norm) bulk_load(at, static_cast<const uint4*>(p.dy) + row, 16 * nvec, bar);
+        if (has_res) bulk_load(at + res_at, static_cast<const char*>(p.dres) + kRes * row, kRes * nvec, bar);
+        if (next_norm) bulk_load(at + h_at, static_cast<const char*>(p.h) + kH * row, kH * nvec, bar);
+        bulk_load(at + x_at, static_cast<const char*>(p.x) + kX * row, kX * nvec, bar);
+        if (scales) bulk_load(at + xs_at, p.x_scales + s0, scales, bar);
+        if (scales && next_norm) bulk_load(at + hs_at, p.h_scales + s0, scales, bar);
+        if (++k == p.depth) {
+          k = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    return;
+  }
+
   bool in[V];
-  Pairs A[V], dw[V], W[kHold ? V : 1], w2[1];
-  Held<PACKED> x_row[V], x_next[V], h_next[V];
+  Pairs A[V], dw[V], W[kHold ? V : 1], w2[kHold ? V : 1];
   auto inner = [&](int v, bool ok) {
     Vec8 a = load_weight(p.post, p.post_f32, v, ok);
     if (p.gate) {
@@ -341,217 +392,172 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
     return pairs(a);
   };
   auto weight_of = [&](int i) {
-    const int v = threadIdx.x + i * blockDim.x;
-    if constexpr (V == 1) return w2[0];
-    else if constexpr (kShared) return pairs(value8<true>(ring8<true>(w_at, v, nvec)));
-    else return pairs(load_weight(p.weight, p.weight_f32, v, true));
+    return kHold ? w2[kHold ? i : 0] : pairs(load_weight(p.weight, p.weight_f32, threadIdx.x + i * threads, true));
   };
-  auto inner_of = [&](int i) { return kHold ? W[kHold ? i : 0] : inner(threadIdx.x + i * blockDim.x, true); };
-  // The row `ahead` of the present one; every read of what is in its place has ended.  A row's scales need
-  // not be whole 16 bytes: those around them are copied, up to the last whole ones of the tensor.
-  auto fetch = [&](int ahead) {
-    if (RING && threadIdx.x == 0 && t + (int64_t)ahead * gridDim.x < T) {
-      const int64_t from = row + ahead * row_step;
-      const uint32_t at = ahead == q.depth ? q.at(0) : q.at(ahead), bar = ahead == q.depth ? q.bar(0) : q.bar(ahead);
-      const int64_t s0 = (from >> 2) & ~(int64_t)15, s1 = min((((from + nvec) >> 2) + 15) & ~(int64_t)15, scale_end);
-      const uint32_t scales = PACKED && s1 > s0 ? (uint32_t)(s1 - s0) : 0;
-      mbar_arrive_expect_tx(bar, xs_at + (next_norm ? 2 : 1) * scales);
-      if (next_norm) bulk_load(at, static_cast<const uint4*>(p.dy) + from, 16 * nvec, bar);
-      if (has_res) bulk_load(at + res_at, static_cast<const char*>(p.dres) + kRes * from, kRes * nvec, bar);
-      if (next_norm) bulk_load(at + h_at, static_cast<const char*>(p.h) + kH * from, kH * nvec, bar);
-      bulk_load(at + x_at, static_cast<const char*>(p.x) + kX * from, kX * nvec, bar);
-      if (scales) bulk_load(at + xs_at, p.x_scales + s0, scales, bar);
-      if (scales && next_norm) bulk_load(at + hs_at, p.h_scales + s0, scales, bar);
-    }
-  };
-  auto read_dy = [&](int64_t from, int ahead, int v) {
-    if constexpr (RING) return row_pairs<false>(q.at(ahead), v);
+  auto inner_of = [&](int i) { return kHold ? W[kHold ? i : 0] : inner(threadIdx.x + i * threads, true); };
+  auto read_dy = [&](int64_t from, uint32_t at, int v) {
+    if constexpr (RING) return row_pairs<false>(at, v);
     else return pairs(load8<false>(p.dy, from + v));
   };
-  auto held = [&](int64_t from, int ahead, uint32_t plane, uint32_t scale_plane, const void* rows, const uint8_t* scales, int v) {
-    Held<PACKED> r{};
-    if constexpr (!PACKED) {
-      if constexpr (RING) r.u = ring16(q.at(ahead) + plane + 16 * v);
-      else r.u = static_cast<const uint4*>(rows)[from + v];
+  auto read_res = [&](int64_t from, uint32_t at, int v) {
+    if constexpr (RING) return row_pairs<F32>(at + res_at, v);
+    else return pairs(load8<F32>(p.dres, from + v));
+  };
+  auto unpacked = [&](int64_t from, uint32_t at, uint32_t scales_at, const void* rows, const uint8_t* scales, int v) {
+    uint2 c;
+    uint32_t byte;
+    if constexpr (RING) {
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(at + 8 * v));
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(scales_at + ((uint32_t)(from >> 2) & 15) + (v >> 2)));
     } else {
-      uint2 c;
-      uint32_t byte;
-      if constexpr (RING) {
-        const int64_t s = from >> 2;
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(q.at(ahead) + plane + 8 * v));
-        if (s + (nvec >> 2) <= scale_end || s + (v >> 2) < scale_end)
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(q.at(ahead) + scale_plane + ((uint32_t)s & 15) + (v >> 2)));
-        else
-          byte = scales[s + (v >> 2)];
-      } else {
-        c = static_cast<const uint2*>(rows)[from + v];
-        byte = scales[(from + v) >> 2];
-      }
-      r.u = e4m3_halves(c);
-      r.s = mx_scale(byte);
+      c = static_cast<const uint2*>(rows)[from + v];
+      byte = scales[(from + v) >> 2];
     }
+    const uint4 u = e4m3_halves(c);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const float2 s = both(mx_scale(byte));
+    Pairs r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.p[j] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&w[j])), s);
     return r;
   };
-  auto read_plain_h = [&](int64_t from, int ahead, int v) {
-    if constexpr (RING) return row_pairs<true>(q.at(ahead) + h_at, v);
-    else return pairs(load8<true>(p.h, from + v));
+  auto read_h = [&](int64_t from, uint32_t at, int v) {
+    if constexpr (PACKED) return unpacked(from, at + h_at, at + hs_at, p.h, p.h_scales, v);
+    else if constexpr (RING) return row_pairs<F32>(at + h_at, v);
+    else return pairs(load8<F32>(p.h, from + v));
   };
-  // this thread's share of a row's sum h^2, sum dy weight h, sum x^2; keeps x and h for the next phases
-  auto sums_of = [&](int64_t from, int ahead, float& hh, float& dot, float& xx) {
-    hh = dot = xx = 0.0f;
+  auto read_x = [&](int64_t from, uint32_t at, int v) {
+    if constexpr (PACKED) return unpacked(from, at + x_at, at + xs_at, p.x, p.x_scales, v);
+    else if constexpr (RING) return row_pairs<false>(at + x_at, v);
+    else return pairs(load8<false>(p.x, from + v));
+  };
+  bool ok = true;  // no wait has run out (rows are then made NaN, not left to chance)
+  // first pass: h h, g h, x x, g W x, h W x, dres W x
+  auto first = [&](int64_t from, uint32_t at, int turn) {
+    float2 s[6];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) s[k] = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (in[i]) {
-        const int v = threadIdx.x + i * blockDim.x;
-        x_next[i] = held(from, ahead, x_at, xs_at, p.x, p.x_scales, v);
-        const Pairs x = x_next[i].value();
-        float2 c = both(0.0f);
+        const int v = threadIdx.x + i * threads;
+        const Pairs x = read_x(from, at, v), w = inner_of(i);
+        Pairs wx;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c = __ffma2_rn(x.p[j], x.p[j], c);
-        xx = fmaf(c.x + c.y, x_next[i].scale() * x_next[i].scale(), xx);
+        for (int j = 0; j < 4; ++j) {
+          s[2] = __ffma2_rn(x.p[j], x.p[j], s[2]);
+          wx.p[j] = __fmul2_rn(x.p[j], w.p[j]);
+        }
         if (next_norm) {
-          Pairs h;
-          float s = 1.0f;
-          if constexpr (kPlainH) {
-            h = read_plain_h(from, ahead, v);
-          } else {
-            h_next[i] = held(from, ahead, h_at, hs_at, p.h, p.h_scales, v);
-            h = h_next[i].value();
-            s = h_next[i].scale();
-          }
-          const Pairs dy = read_dy(from, ahead, v), w = weight_of(i);
-          float2 a = both(0.0f), b = both(0.0f);
+          const Pairs h = read_h(from, at, v), dy = read_dy(from, at, v), u = weight_of(i);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            a = __ffma2_rn(h.p[j], h.p[j], a);
-            b = __ffma2_rn(h.p[j], __fmul2_rn(dy.p[j], w.p[j]), b);
+            const float2 g = __fmul2_rn(dy.p[j], u.p[j]);
+            s[0] = __ffma2_rn(h.p[j], h.p[j], s[0]);
+            s[1] = __ffma2_rn(h.p[j], g, s[1]);
+            s[3] = __ffma2_rn(g, wx.p[j], s[3]);
+            s[4] = __ffma2_rn(h.p[j], wx.p[j], s[4]);
           }
-          hh = fmaf(a.x + a.y, s * s, hh);
-          dot = fmaf(b.x + b.y, s, dot);
+        }
+        if (has_res) {
+          const Pairs r = read_res(from, at, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[5] = __ffma2_rn(r.p[j], wx.p[j], s[5]);
         }
       }
     }
-    if (!q.ok) xx = NAN;
+    float a[8];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) a[k] = s[k].x + s[k].y;
+    a[6] = a[7] = 0.0f;
+    if (!ok) a[2] = NAN;
+    put_sums(a, smem[turn], warp);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(exchange);
   };
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    in[i] = i < V - 1 || threadIdx.x + i * blockDim.x < nvec;  // only the last can be past the row
-    x_row[i] = x_next[i] = h_next[i] = Held<PACKED>{};
+    in[i] = i < V - 1 || (int)threadIdx.x + i * threads < nvec;  // only the last can be past the row
 #pragma unroll
     for (int j = 0; j < 4; ++j) A[i].p[j] = dw[i].p[j] = both(0.0f);
   }
-  if (RING && threadIdx.x == 0) {
-    for (int k = 0; k < p.depth; ++k) mbar_init(q.bars + 8 * k, 1);
-    s_abort = 0;
-    fence_barrier_init();
-  }
-  for (int i = threadIdx.x; i < 128; i += blockDim.x) (&smem[0][0][0])[i] = 0.0f;
-  __syncthreads();
-  for (int k = 0; k < p.depth; ++k) fetch(k);
 #pragma unroll
   for (int i = 0; i < (kHold ? V : 0); ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
+    const int v = threadIdx.x + i * threads;
     W[i] = inner(v, in[i]);
-    const Vec8 w = next_norm ? load_weight(p.weight, p.weight_f32, v, in[i]) : Vec8{};
-    if constexpr (V == 1) {
-      w2[0] = pairs(w);
-    } else if (in[i]) {  // read back by this thread alone
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(w_at + 16 * v), "f"(w.v[0]), "f"(w.v[1]), "f"(w.v[2]), "f"(w.v[3]) : "memory");
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(w_at + 16 * (nvec + v)), "f"(w.v[4]), "f"(w.v[5]), "f"(w.v[6]), "f"(w.v[7]) : "memory");
-    }
+    w2[i] = pairs(next_norm ? load_weight(p.weight, p.weight_f32, v, in[i]) : Vec8{});
   }
   float gate = p.token_gate ? p.token_gate[t] : 1.0f, next_gate = 1.0f;
-  float sums[4];  // h^2, dy weight h, x^2 of the next row; ds W x of this one
-  if constexpr (RING) q.wait(0, &s_abort);
-  sums_of(row, 0, sums[0], sums[1], sums[2]);
-  sums[3] = 0.0f;
-  row_sums(sums, smem, 1);
+  float sums[6];
   const float2 a2 = both(p.res_scale);
-  for (int turn = 0; t < T; turn ^= 1) {
+  uint32_t at = base, phase = 0;  // the row's place in the ring and its phase
+  int k = 0, turn = 0;
+  if constexpr (RING) ok &= mbar_wait(full, 0, nullptr, &s_abort);
+  first(row, at, 0);
+  ok &= mbar_wait(exchange, 0, nullptr, &s_abort);
+  get_sums(sums, smem[0]);
+  while (true) {
     const bool more = t + (int)gridDim.x < T;
-    if (p.token_gate && more) next_gate = p.token_gate[t + gridDim.x];
+    const int next_k = k + 1 == p.depth ? 0 : k + 1;
+    const uint32_t next_phase = next_k ? phase : phase ^ 1, next_at = base + next_k * place;
+    turn ^= 1;
+    auto ahead = [&]() {
+      if (!more) return;
+      if (p.token_gate) next_gate = p.token_gate[t + gridDim.x];
+      if constexpr (RING) ok &= mbar_wait(full + 8 * next_k, next_phase, nullptr, &s_abort);
+      first(row + row_step, next_at, turn);
+    };
+    if constexpr (!kLate) ahead();
     const float rho1 = rsqrtf(fmaf(sums[2], p.inv_d, p.eps)), rho2 = rsqrtf(fmaf(sums[0], p.inv_d, p.eps));
-    const float c2 = -sums[1] * p.inv_d * rho2 * rho2, rt = rho1 * gate;  // - mean(g hhat) rho2
-    const float2 r2 = both(rho2);
-    Pairs ds[V];
-    float qx = 0.0f;
+    const float c2 = -sums[1] * p.inv_d * rho2 * rho2;  // - mean(g hhat) rho2
+    const float q = fmaf(rho2, fmaf(c2, sums[4], sums[3]), sums[5]);
+    const float2 r2 = both(rho2), cc2 = both(c2), rt = both(rho1 * gate), c1 = both(-q * p.inv_d * rho1 * rho1);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
       if (in[i]) {
-        ds[i] = Pairs{};
-        if (has_res) {
-          if constexpr (RING) ds[i] = row_pairs<F32>(q.at(0) + res_at, v);
-          else ds[i] = pairs(load8<F32>(p.dres, row + v));
-        }
+        const int v = threadIdx.x + i * threads;
+        Pairs ds = has_res ? read_res(row, at, v) : Pairs{}, o;
         if (next_norm) {
-          Pairs h;
-          float s = 1.0f;
-          if constexpr (kPlainH) {
-            h = read_plain_h(row, 0, v);
-          } else {
-            h = h_next[i].value();
-            s = h_next[i].scale();
-          }
-          const Pairs dy = read_dy(row, 0, v), w = weight_of(i);
-          const float2 rs = both(rho2 * s), cs = both(c2 * s);
+          const Pairs h = read_h(row, at, v), dy = read_dy(row, at, v), u = weight_of(i);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            dw[i].p[j] = __ffma2_rn(dy.p[j], __fmul2_rn(h.p[j], rs), dw[i].p[j]);
-            const float2 g = __ffma2_rn(h.p[j], cs, __fmul2_rn(dy.p[j], w.p[j]));
-            ds[i].p[j] = __ffma2_rn(g, r2, ds[i].p[j]);
+            dw[i].p[j] = __ffma2_rn(dy.p[j], __fmul2_rn(h.p[j], r2), dw[i].p[j]);
+            ds.p[j] = __ffma2_rn(__ffma2_rn(h.p[j], cc2, __fmul2_rn(dy.p[j], u.p[j])), r2, ds.p[j]);
           }
         }
-        x_row[i] = x_next[i];
-        const Pairs x = x_row[i].value(), w = inner_of(i);
-        const float2 rs = both(rt * x_row[i].scale());
-        float2 qs = both(0.0f);
-        Pairs o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.p[j] = __fmul2_rn(ds.p[j], a2);
+        store_pairs<F32>(p.dresidual, row + v, o);
+        const Pairs x = read_x(row, at, v), w = inner_of(i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 dx = __fmul2_rn(ds[i].p[j], x.p[j]);
-          A[i].p[j] = __ffma2_rn(dx, rs, A[i].p[j]);
-          qs = __ffma2_rn(dx, w.p[j], qs);
-          o.p[j] = __fmul2_rn(ds[i].p[j], a2);
+          A[i].p[j] = __ffma2_rn(__fmul2_rn(ds.p[j], x.p[j]), rt, A[i].p[j]);
+          o.p[j] = __fmul2_rn(__ffma2_rn(x.p[j], c1, __fmul2_rn(ds.p[j], w.p[j])), rt);
         }
-        qx = fmaf(qs.x + qs.y, x_row[i].scale(), qx);
-        store_pairs<F32>(p.dresidual, row + v, o);
-      }
-    }
-    sums[0] = sums[1] = sums[2] = 0.0f;
-    if (more) {
-      if constexpr (RING) q.wait(1, &s_abort);
-      sums_of(row + row_step, 1, sums[0], sums[1], sums[2]);
-    }
-    sums[3] = qx;
-    row_sums(sums, smem, turn);
-    if (blockDim.x == 32) __syncwarp();
-    fetch(q.depth);  // into this row's place
-    const float c1 = -sums[3] * p.inv_d * rho1 * rho1;  // - mean(ds W xhat) rho1
-    const float2 rt2 = both(rt);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (in[i]) {
-        const Pairs x = x_row[i].value(), w = inner_of(i);
-        const float2 cs = both(c1 * x_row[i].scale());
-        Pairs o;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o.p[j] = __fmul2_rn(__ffma2_rn(x.p[j], cs, __fmul2_rn(ds[i].p[j], w.p[j])), rt2);
         store_pairs<false>(p.dx, row + v, o);
       }
     }
-    if (p.dtoken_gate && threadIdx.x == 0) p.dtoken_gate[t] = rho1 * sums[3];
+    if (p.dtoken_gate && threadIdx.x == 0) p.dtoken_gate[t] = rho1 * q;
+    if constexpr (RING) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * k);
+    }
+    if constexpr (kLate) ahead();
+    if (!more) break;
+    ok &= mbar_wait(exchange, turn, nullptr, &s_abort);
+    get_sums(sums, smem[turn]);
     gate = next_gate;
     t += gridDim.x;
     row += row_step;
-    q.next();
+    k = next_k;
+    phase = next_phase;
+    at = next_at;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   float* mine = p.partial + (int64_t)blockIdx.x * p.d;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
+    const int v = threadIdx.x + i * threads;
     if (in[i]) {
       store_pairs<true>(mine, v, A[i]);
       if (next_norm) store_pairs<true>(mine + (int64_t)gridDim.x * p.d, v, dw[i]);
@@ -645,15 +651,21 @@ static SandwichShape sandwich_shape(int d, bool warp_rows, int per_sm) {
   return n;
 }
 constexpr int kThreadsPerSm = 512;  // 128 registers each
-static int sandwich_bwd_grid(int sms, int64_t T, int d) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(T, (int64_t)sms * sandwich_shape(d, false, kThreadsPerSm).blocks));
+// Backward: one of the warps fetches (not for the widest rows, which have no ring).
+static SandwichShape sandwich_bwd_shape(int d) {
+  SandwichShape n = sandwich_shape(d, false, kThreadsPerSm - 32);
+  n.blocks = std::max(1, std::min(kThreadsPerSm / (n.threads + 32), 8));
+  return n;
 }
-// Places of the ring for the rows that a block has to take, three or two; 0 where they do not fit beside
-// `more` bytes, and for the widest rows (they are then read from memory, the second time from L2).
-static int ring_depth(int64_t turns, int blocks, int64_t bytes, int64_t more, int v) {
+static int sandwich_bwd_grid(int sms, int64_t T, int d) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(T, (int64_t)sms * sandwich_bwd_shape(d).blocks));
+}
+// Places of the ring for the rows that a block has to take, three or (`two`) two; 0 where they do not fit and
+// for the widest rows (they are then read from memory, the second time from L2).
+static int ring_depth(int64_t turns, int blocks, int64_t bytes, int v, bool two) {
   if (v > 4) return 0;
-  const int64_t room = kSmemPerSm / blocks - kSmemOwn - more;
-  for (int depth = 3; depth >= 2; --depth)
+  const int64_t room = kSmemPerSm / blocks - kSmemOwn;
+  for (int depth = 3; depth >= (two ? 2 : 3); --depth)
     if (std::min<int64_t>(depth, turns) * bytes <= room) return (int)std::min<int64_t>(depth, turns);
   return 0;
 }
@@ -701,7 +713,7 @@ int mok_sandwich_norm(const mok_sandwich* a, int64_t T, int d, const void* x, co
   const int64_t row_bytes = 2 * d * (f32 ? 3 : 2);
   const int64_t groups = (p.rows + n.rows - 1) / n.rows, most = (int64_t)sms * n.blocks;
   const int grid = (int)std::min<int64_t>(groups, most);
-  p.depth = ring_depth((T + (int64_t)grid * n.rows - 1) / ((int64_t)grid * n.rows), n.blocks, n.rows * row_bytes, 0, n.v);
+  p.depth = ring_depth((T + (int64_t)grid * n.rows - 1) / ((int64_t)grid * n.rows), n.blocks, n.rows * row_bytes, n.v, true);
   const int64_t smem = p.depth * n.rows * row_bytes;
   void (*k)(const SandwichParams) = nullptr;
   auto pick = [&](auto type, auto ring) {
@@ -767,18 +779,17 @@ int mok_sandwich_norm_backward(const mok_sandwich* a, int64_t T, int d, const vo
                       a->post_weight, a->gate, a->token_gate, a->weight, dx, dresidual, dtoken_gate, partial, T, d, a->eps,
                       1.0f / (float)d, a->res_scale, a->post_type == MOK_T_F32, a->gate_type == MOK_T_F32,
                       a->weight_type == MOK_T_F32, 0};
-  const SandwichShape n = sandwich_shape(d, false, kThreadsPerSm);
+  const SandwichShape n = sandwich_bwd_shape(d);
   const int64_t nvec = d / 8, res = f32 ? 32 : 16;
   const int64_t scales = packed ? (nvec / 4 + 31) / 16 * 16 : 0;  // as the kernel lays a place out
   const int64_t row_bytes = nvec * ((dy ? 16 : 0) + (dres ? res : 0) + (dy ? (packed ? 8 : res) : 0) + (packed ? 8 : 16)) + scales * (dy ? 2 : 1);
-  const int64_t own = n.v == 2 ? 4 * d : 0;  // the next norm's weight
-  p.depth = ring_depth((T + grid - 1) / grid, n.blocks, row_bytes, own, n.v);
-  const int64_t smem = p.depth * row_bytes + own;
+  p.depth = ring_depth((T + grid - 1) / grid, n.blocks, row_bytes, n.v, f32 && !packed);
+  const int64_t smem = p.depth * row_bytes;
   void (*k)(const SandwichBwdParams) = nullptr;
   auto pick = [&](auto type, auto codes, auto ring) {
     constexpr bool F = decltype(type)::value, C = decltype(codes)::value, R = decltype(ring)::value;
-    k = n.v == 1 ? sandwich_bwd_kernel<1, F, C, R, 512> : n.v == 2 ? sandwich_bwd_kernel<2, F, C, R, 512>
-        : n.v == 4 ? sandwich_bwd_kernel<4, F, C, R, 512> : sandwich_bwd_kernel<8, F, C, false, 512>;
+    k = n.v == 1 ? sandwich_bwd_kernel<1, F, C, R, kThreadsPerSm> : n.v == 2 ? sandwich_bwd_kernel<2, F, C, R, kThreadsPerSm>
+        : n.v == 4 ? sandwich_bwd_kernel<4, F, C, R, kThreadsPerSm> : sandwich_bwd_kernel<8, F, C, false, kThreadsPerSm>;
   };
   auto pick2 = [&](auto type, auto codes) {
     if (p.depth) pick(type, codes, std::true_type{});
@@ -790,7 +801,7 @@ int mok_sandwich_norm_backward(const mok_sandwich* a, int64_t T, int d, const vo
   else pick2(std::false_type{}, std::false_type{});
   if (allow_smem(k, smem) != cudaSuccess) return MOK_ERR_CUDA;
   prof_begin("sandwich_bwd", st);
-  k<<<grid, n.threads, smem, st>>>(p);
+  k<<<grid, n.threads + (p.depth ? 32 : 0), smem, st>>>(p);
   prof_end(st);
   if (cudaGetLastError() != cudaSuccess) return MOK_ERR_CUDA;
   const SandwichSumParams sp{partial, grid, d, a->post_weight, a->gate, dpost_weight, dgate, dweight, p.post_f32, p.gate_f32};
