@@ -114,7 +114,7 @@ __device__ __forceinline__ Pairs row_pairs(uint32_t at, int v) {  // vector v of
 
 // V vectors of eight per thread, MT threads at most.
 template <int V, bool F32, bool RING, int MT>
-__global__ void __launch_bounds__(MT) sandwich_kernel(const __grid_constant__ SandwichParams p) {
+__global__ void __launch_bounds__(MT, V == 1 ? 2 : 1) sandwich_kernel(const __grid_constant__ SandwichParams p) {
   __shared__ float smem[2][2][16];
   __shared__ __align__(8) uint64_t bars[8][3];
   __shared__ int s_abort;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
   int t = blockIdx.x;  // gridDim.x <= T
   int64_t row = (int64_t)t * nvec;  // vectors before the row
   const int64_t row_step = (int64_t)gridDim.x * nvec;
-  constexpr bool kHold = V <= 2;  // the weights in registers; else they are read where they are used
+  constexpr bool kHold = V <= 3;  // the weights in registers; else they are read where they are used
   constexpr bool kLate = F32 && !PACKED;
   const bool next_norm = p.dy != nullptr, has_res = p.dres != nullptr;
   // planes of a place: dy, dres, h, x, and for codes the two tensors' scales
@@ -641,20 +641,29 @@ struct SandwichShape {
 constexpr int kSmemPerSm = 227 * 1024;  // for the blocks of an SM together
 constexpr int kSmemOwn = 3072;          // of a block: reserved and static
 constexpr int kPlainSmem = 40 * 1024;   // dynamic bytes that need no attribute
-static SandwichShape sandwich_shape(int d, bool warp_rows, int per_sm) {
+constexpr int kWideThreads = 512;       // of a block with two vectors per thread and more: 128 registers each
+// Forward: one vector per thread up to 512 threads, of which 1024 fit an SM (64 registers).
+static SandwichShape sandwich_shape(int d) {
   SandwichShape n;
   const int nvec = d / 8;
-  n.v = nvec <= per_sm ? 1 : nvec <= 2 * per_sm ? 2 : nvec <= 4 * per_sm ? 4 : 8;
+  n.v = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8;
   n.threads = ((nvec + n.v - 1) / n.v + 31) / 32 * 32;
-  n.rows = warp_rows && n.threads == 32 ? 8 : 1;
-  n.blocks = std::max(1, std::min(per_sm / (n.threads * n.rows), 8));
+  n.rows = n.threads == 32 ? 8 : 1;
+  n.blocks = n.v == 1 ? std::max(1, std::min(1024 / (n.threads * n.rows), 8)) : 1;
   return n;
 }
-constexpr int kThreadsPerSm = 512;  // 128 registers each
-// Backward: one of the warps fetches (not for the widest rows, which have no ring).
+// Backward: one warp more fetches (not for the widest rows, which have no ring).  A vector of a thread
+// takes 32 registers across rows (two weights, two sums), so threads get 96 registers with one vector, 128
+// with two, 168 with three, and with that warp a block has no more threads than those allow.
+constexpr int kNarrowThreads = 512 + 32, kThreeThreads = 384;
 static SandwichShape sandwich_bwd_shape(int d) {
-  SandwichShape n = sandwich_shape(d, false, kThreadsPerSm - 32);
-  n.blocks = std::max(1, std::min(kThreadsPerSm / (n.threads + 32), 8));
+  SandwichShape n;
+  const int nvec = d / 8;
+  n.v = nvec <= 512 ? 1 : nvec <= 2 * (kWideThreads - 32) ? 2 : nvec <= 3 * (kThreeThreads - 32) ? 3
+      : nvec <= 4 * (kWideThreads - 32) ? 4 : 8;
+  n.threads = ((nvec + n.v - 1) / n.v + 31) / 32 * 32;
+  n.rows = 1;
+  n.blocks = n.v == 1 ? std::max(1, std::min(65536 / 96 / (n.threads + 32), 8)) : 1;
   return n;
 }
 static int sandwich_bwd_grid(int sms, int64_t T, int d) {
@@ -709,7 +718,7 @@ int mok_sandwich_norm(const mok_sandwich* a, int64_t T, int d, const void* x, co
                    scale_layout == MOK_SCALES_ATOMS, 0};
   if (codes && p.atoms) p.rows = (T + 127) / 128 * 128;
   const int sms = num_sms();
-  const SandwichShape n = sandwich_shape(d, true, kThreadsPerSm);
+  const SandwichShape n = sandwich_shape(d);
   const int64_t row_bytes = 2 * d * (f32 ? 3 : 2);
   const int64_t groups = (p.rows + n.rows - 1) / n.rows, most = (int64_t)sms * n.blocks;
   const int grid = (int)std::min<int64_t>(groups, most);
@@ -788,8 +797,9 @@ int mok_sandwich_norm_backward(const mok_sandwich* a, int64_t T, int d, const vo
   void (*k)(const SandwichBwdParams) = nullptr;
   auto pick = [&](auto type, auto codes, auto ring) {
     constexpr bool F = decltype(type)::value, C = decltype(codes)::value, R = decltype(ring)::value;
-    k = n.v == 1 ? sandwich_bwd_kernel<1, F, C, R, kThreadsPerSm> : n.v == 2 ? sandwich_bwd_kernel<2, F, C, R, kThreadsPerSm>
-        : n.v == 4 ? sandwich_bwd_kernel<4, F, C, R, kThreadsPerSm> : sandwich_bwd_kernel<8, F, C, false, kThreadsPerSm>;
+    k = n.v == 1 ? sandwich_bwd_kernel<1, F, C, R, kNarrowThreads> : n.v == 2 ? sandwich_bwd_kernel<2, F, C, R, kWideThreads>
+        : n.v == 3 ? sandwich_bwd_kernel<3, F, C, R, kThreeThreads> : n.v == 4 ? sandwich_bwd_kernel<4, F, C, R, kWideThreads>
+        : sandwich_bwd_kernel<8, F, C, false, kWideThreads>;
   };
   auto pick2 = [&](auto type, auto codes) {
     if (p.depth) pick(type, codes, std::true_type{});

@@ -58,7 +58,7 @@ def _packed(t):
             q.double().numpy() * np.repeat(2.0 ** s, 32, axis=-1))
 
 
-CASES = [(1, 8, "bf16", "bf16", "none"), (1, 7168, "bf16", "bf16", "none"), (3, 256, "f32", "bf16", "both"),
+CASES = [(311, 8192, "bf16", "bf16", "channel"), (5, 8448, "f32", "f32", "both"), (1, 8, "bf16", "bf16", "none"), (1, 7168, "bf16", "bf16", "none"), (3, 256, "f32", "bf16", "both"),
          (9, 264, "bf16", "f32", "channel"), (700, 64, "bf16", "bf16", "token"), (517, 1544, "f32", "f32", "both"),
          (400, 4096, "bf16", "bf16", "channel"), (330, 7168, "f32", "bf16", "token"), (7, 8200, "bf16", "f32", "both"),
          (310, 16384, "bf16", "bf16", "none"), (5, 16392, "f32", "f32", "both"), (157, 32768, "bf16", "bf16", "token"),
