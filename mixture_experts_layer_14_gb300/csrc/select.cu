@@ -5,12 +5,12 @@
 //   w_j = scale s_j / sum s_i (or scale s_j).
 //
 // A warp takes a token, a lane a run of neighbouring experts of one group, in ascending order.  The
-// k-th largest of the lanes' own largest keys is a lower limit of the k-th key, which leaves about
-// k + 2 candidates (their expected number, 32 (H(32) - H(32 - k)), is 9.1 for k = 8); these go
-// to a lane each and are ranked by counting.  Which of two experts is chosen is decided as in exact
-// arithmetic: where two keys that the choice depends on are nearer than fp32 can tell (a few tokens
-// in a thousand) the experts in question are ranked again in 64 bits.  Without a bias scores rise
-// with the logits, which are ranked themselves.
+// lanes' largest keys are dealt into S >= k sets (a power of two), and the least of the sets' largest
+// is a lower limit of the k-th key, which leaves S H(S) candidates in the mean (22 for k = 8); these go to
+// a lane each and are ranked by counting.  Which of two experts is chosen is decided as in exact
+// arithmetic: where two keys that the choice depends on are nearer than fp32 can tell (a few tokens in a
+// thousand) the experts in question are ranked again in 64 bits.  Without a bias scores rise with the
+// logits, which are ranked themselves.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -35,6 +35,7 @@ struct SelectParams {
   int groups, kept, n;     // groups, how many stay, experts of one
   int lanes, log_lanes;    // of a group: a power of two
   int chunk;               // experts of a lane
+  int sets;                // least power of two >= k
   int top2, renorm;
   float scale;
 };
@@ -84,16 +85,17 @@ struct SelectRow {
   __device__ __forceinline__ float error() const {
     return score(top) * (SOFTMAX ? 0x1p-17f : fmaf(0x1p-22f, fmaxf(-top, 0.0f), 0x1p-20f)) + 1e-37f;
   }
-  __device__ __forceinline__ float open_bias(int e) const {
-    if constexpr (!BIAS) return 0.0f;
-    const float b = bias[e];
-    return fabsf(b) < -kShutOff ? b : -INFINITY;
-  }
+  __device__ __forceinline__ float bias_of(int e) const { return BIAS ? bias[e] : 0.0f; }
   // What experts are ranked by, and what groups are.
   __device__ __forceinline__ float key(float l, float b) const {
-    return l > kShutOff ? (BIAS ? fmaxf(score(l) + b, kMasked) : l) : kMasked;
+    if constexpr (!BIAS) return l > kShutOff ? l : kMasked;
+    const float c = score(l) + b;
+    return l > kShutOff && fabsf(b) < -kShutOff ? c : kMasked;
   }
-  __device__ __forceinline__ float group_key(float l, float b) const { return l > kShutOff ? score(l) + b : -INFINITY; }
+  __device__ __forceinline__ float group_key(float l, float b) const {
+    const float c = score(l) + b;
+    return l > kShutOff && (!BIAS || fabsf(b) < -kShutOff) ? c : -INFINITY;
+  }
 };
 
 // Key of expert e in 64 bits; sum: of exp(l - top), for softmax with a bias.
@@ -115,9 +117,8 @@ __device__ __noinline__ double exact_sum(SelectRow<SOFTMAX, BIAS> r, int E) {
 }
 
 // The k best experts of [lo, hi) in exact order among those with keys[e] >= threshold (k <= 8);
-// lane j < k returns the j-th (index -1: there is none).  `list` holds hi - lo numbers.  The
-// candidates are packed 24 to a round beside the best so far, so that the usual handful takes one
-// evaluation in 64 bits.
+// lane j < k returns the j-th (index -1: there is none).  `list` holds hi - lo numbers.  Up to 32 are
+// ranked by counting; more of them (many equal numbers) come 24 to a round beside the best so far.
 template <bool SOFTMAX, bool BIAS>
 __device__ __noinline__ int exact_best(SelectRow<SOFTMAX, BIAS> r, double sum, const float* keys, int* list, int lo, int hi,
                                        float threshold, int k, double* key_out) {
@@ -133,6 +134,26 @@ __device__ __noinline__ int exact_best(SelectRow<SOFTMAX, BIAS> r, double sum, c
   __syncwarp();
   int idx = -1;
   double key = 0.0;
+  if (count <= 32) {  // a lane each, in ascending order
+    if (lane < count) {
+      idx = list[lane];
+      key = exact_key(r, sum, idx, keys[idx]);
+    }
+    int place = 0;
+    for (int j = 0; j < count; ++j) {
+      const double o = __shfl_sync(kAll, key, j);
+      place += o > key || (o == key && j < lane);
+    }
+    __syncwarp();
+    if (lane < count) list[place] = lane;
+    __syncwarp();
+    const int from = lane < min(k, count) ? list[lane] : -1;
+    const int i = __shfl_sync(kAll, idx, max(from, 0));
+    const double d = __shfl_sync(kAll, key, max(from, 0));
+    __syncwarp();
+    *key_out = d;
+    return from < 0 ? -1 : i;
+  }
   for (int at = 0; at < count; at += 24) {
     if (lane >= 8) {
       idx = at + lane - 8 < count ? list[at + lane - 8] : -1;
@@ -166,7 +187,7 @@ template <bool SOFTMAX, bool BIAS>
 __device__ __noinline__ bool exact_groups(SelectRow<SOFTMAX, BIAS> r, const SelectParams& p, float* keys, int* list, float err,
                                           float score, float second, float in, float out, float slack) {
   const int lane = threadIdx.x & 31, group = lane >> p.log_lanes;
-  for (int e = lane; e < p.E; e += 32) keys[e] = r.group_key(r.logits[e], r.open_bias(e));
+  for (int e = lane; e < p.E; e += 32) keys[e] = r.group_key(r.logits[e], r.bias_of(e));
   const double sum = exact_sum(r, p.E);
   __syncwarp();
   double mine = score > -INFINITY ? (double)score : -1e300;
@@ -238,14 +259,9 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_ker
     bad |= c[i] != c[i];
     top = fmaxf(top, c[i]);  // passes NaN by
   }
-  if constexpr (BIAS) {
-    if (t == 0) {  // the same for every token
+  if (BIAS && t == 0) {  // the same for every token
 #pragma unroll
-      for (int i = 0; i < V; ++i) bad |= !(b[i] < -kShutOff);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!(fabsf(b[i]) < -kShutOff)) b[i] = -INFINITY;
+    for (int i = 0; i < V; ++i) bad |= !(b[i] < -kShutOff);
   }
   if (__any_sync(kAll, bad) && lane == 0) record_status(p.status, MOK_ERR_DEVICE_CHECK);
 
@@ -296,19 +312,23 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_ker
     c[i] = i < own && stays ? r.key(c[i], b[i]) : kAbsent;
     best = fmaxf(best, c[i]);
   }
-  // The `want`-th largest of the lanes' largest keys (one more than k where the next one matters).
-  const int want = BIAS ? p.k + 1 : p.k;
-  float limit = kAbsent;
-  for (int j = 0; j < want; ++j) {
-    limit = warp_top(best);
-    const unsigned at = __ballot_sync(kAll, best == limit);
-    if (lane == __ffs(at) - 1) best = kAbsent;
+  // The lower limit.  Lanes without experts would leave their set empty: the others are moved up first.
+  const int want = BIAS ? p.k + 1 : p.k;  // one more than k where the next one matters
+  const unsigned busy = __ballot_sync(kAll, best > kAbsent);
+  if (busy != kAll) {
+    if (best > kAbsent) keys[__popc(busy & ((1u << lane) - 1u))] = best;
+    __syncwarp();
+    best = lane < __popc(busy) ? keys[lane] : kAbsent;
+    __syncwarp();
   }
-  // Candidates in ascending order: keys at the limit or above, all of them where there are fewer lanes
-  // than wanted.  Beyond 32 of them, of those at the limit the first `want`, behind the others.
-  unsigned mine = 0, equal = 0;
+  float limit = best;
+  for (int o = 16; o >= p.sets; o >>= 1) limit = fmaxf(limit, __shfl_xor_sync(kAll, limit, o));
+  for (int o = p.sets >> 1; o; o >>= 1) limit = fminf(limit, __shfl_xor_sync(kAll, limit, o));
+  // Candidates in ascending order: open experts with keys at the limit or above.  Beyond 32 of them, of
+  // those at the limit only the first `want`, behind the others; fewer than k, shut off ones behind them.
+  unsigned mine = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) mine |= (c[i] >= limit && c[i] > kAbsent ? 1u : 0u) << i;
+  for (int i = 0; i < V; ++i) mine |= (c[i] >= limit && c[i] > kMasked ? 1u : 0u) << i;
   auto scan = [&](unsigned v) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -320,9 +340,11 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_ker
   unsigned upto = scan(__popc(mine));
   int n = (int)__shfl_sync(kAll, upto, 31);
   int at = (int)upto - __popc(mine);
-  if (n > 32) {
+  if ((n > 32 && limit > kMasked) || n < p.k) {
+    const float rest = n < p.k ? kMasked : limit;
+    unsigned equal = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) equal |= (c[i] == limit && c[i] > kAbsent ? 1u : 0u) << i;
+    for (int i = 0; i < V; ++i) equal |= (c[i] == rest ? 1u : 0u) << i;
     mine &= ~equal;
     const unsigned two = __popc(mine) | __popc(equal) << 16;
     upto = scan(two);
@@ -334,19 +356,24 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_ker
   }
   for (; mine; mine &= mine - 1) list[at++] = first + __ffs(mine) - 1;
   __syncwarp();
-  // A lane per candidate: its key once more, then its place in the order.
+  // A lane per candidate: its key once more, then its place in the order: the number of larger ones, and
+  // of equal ones before it.
+  if (lane <= kMaxK) s_idx[warp][lane] = 0;
   for (int q = lane; q < (n + 3) / 4 * 4; q += 32)
-    keys[q] = q < n ? r.key(row[list[q]], r.open_bias(list[q])) : kAbsent;
+    keys[q] = q < n ? r.key(row[list[q]], r.bias_of(list[q])) + 0.0f : kAbsent;  // one zero
   __syncwarp();
   for (int q = lane; q < n; q += 32) {
     const float key = keys[q];
     int place = 0;
     for (int j = 0; j < n; j += 4) {
       const float4 o = *reinterpret_cast<const float4*>(keys + j);
-      place += o.x > key || (o.x == key && j < q);
-      place += o.y > key || (o.y == key && j + 1 < q);
-      place += o.z > key || (o.z == key && j + 2 < q);
-      place += o.w > key || (o.w == key && j + 3 < q);
+      place += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
+    }
+    if (n <= 32) {  // the lanes below n, once
+      const unsigned here = n == 32 ? kAll : (1u << n) - 1u;
+      place += __popc(__match_any_sync(here, __float_as_uint(key)) & ((1u << lane) - 1u));
+    } else {
+      for (int j = 0; j < q; ++j) place += keys[j] == key;
     }
     if (place < want) {
       s_key[warp][place] = key;
@@ -355,7 +382,8 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_ker
   }
   __syncwarp();
   int idx = lane < min(want, n) ? s_idx[warp][lane] : 0;  // n >= k
-  const float key = lane < min(want, n) ? s_key[warp][lane] : kAbsent;
+  // without a further candidate nothing that is not chosen exceeds the limit
+  const float key = lane < min(want, n) ? s_key[warp][lane] : lane == n ? limit : kAbsent;
   if constexpr (BIAS) {
     // Neighbours in the order that are nearer than their errors, unless they are one and the same
     // number; such a pair at the border may have others as near behind it.
@@ -372,7 +400,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_ker
     if (__shfl_sync(kAll, (int)tie, p.k - 1)) {
 #pragma unroll 1
       for (int e = first; e < first + own; ++e) {
-        const float y = r.key(row[e], r.open_bias(e));
+        const float y = r.key(row[e], r.bias_of(e));
         unsure |= stays && y > kMasked && (y < last || (y == last && e > last_idx)) && near(last, y) &&
                   !(row[e] == row[last_idx] && p.bias[e] == p.bias[last_idx]);
       }
@@ -387,6 +415,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_ker
       // kMasked: fewer than k are open
       idx = exact_best(r, total, keys, list, 0, p.E,
                        last == kMasked ? kMasked : fmaxf(last - 2.0f * err - 0x1p-22f * fabsf(last), kMasked), p.k, &d);
+      idx = max(idx, 0);
     }
   }
   // weights: lane j has its own logit
@@ -571,12 +600,13 @@ int mok_select_experts(const mok_dims* dims, const mok_selection* sel, const flo
   set_last_launches(0);
   if (dims->T == 0) return MOK_OK;
   SelectParams p{logits, sel_bias, topk_idx, topk_w, static_cast<int*>(ws), dims->T, dims->E, dims->k, sel->n_groups,
-                 sel->topk_groups, dims->E / sel->n_groups, 1, 0, 0,
+                 sel->topk_groups, dims->E / sel->n_groups, 1, 0, 0, 1,
                  sel->group_score == MOK_GROUP_TOP2, sel->renormalise != 0, sel->scale};
   while (2 * p.lanes * p.groups <= 32) {
     p.lanes *= 2;
     ++p.log_lanes;
   }
+  while (p.sets < dims->k) p.sets *= 2;
   p.chunk = (p.n + p.lanes - 1) / p.lanes;  // at most 30: E <= 512
   const bool vec = p.n % 4 == 0;
   if (vec) p.chunk = (p.chunk + 3) / 4 * 4;
