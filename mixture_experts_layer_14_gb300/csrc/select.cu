@@ -35,7 +35,7 @@ struct SelectParams {
   int groups, kept, n;     // groups, how many stay, experts of one
   int lanes, log_lanes;    // of a group: a power of two
   int chunk;               // experts of a lane
-  int sets;                // least power of two >= k
+  int sets;                // a power of two, at least k
   int top2, renorm;
   float scale;
 };
@@ -606,7 +606,9 @@ int mok_select_experts(const mok_dims* dims, const mok_selection* sel, const flo
     p.lanes *= 2;
     ++p.log_lanes;
   }
-  while (p.sets < dims->k) p.sets *= 2;
+  // one set more than k, so that the next key is mostly among the candidates; for k = 8 it is with 8 sets
+  // too, but for one token in 400 (8! / 8^8)
+  while (p.sets < std::min(dims->k + (sel_bias ? 1 : 0), 8)) p.sets *= 2;
   p.chunk = (p.n + p.lanes - 1) / p.lanes;  // at most 30: E <= 512
   const bool vec = p.n % 4 == 0;
   if (vec) p.chunk = (p.chunk + 3) / 4 * 4;
