@@ -5,12 +5,12 @@
 //   w_j = scale s_j / sum s_i (or scale s_j).
 //
 // A warp takes a token, a lane a run of neighbouring experts of one group, in ascending order.  The
-// lanes' largest keys are dealt into S >= k sets (a power of two), and the least of the sets' largest
-// is a lower limit of the k-th key, which leaves S H(S) candidates in the mean (22 for k = 8); these go to
-// a lane each and are ranked by counting.  Which of two experts is chosen is decided as in exact
-// arithmetic: where two keys that the choice depends on are nearer than fp32 can tell (a few tokens in a
-// thousand) the experts in question are ranked again in 64 bits.  Without a bias scores rise with the
-// logits, which are ranked themselves.
+// k-th largest of the lanes' own largest keys is a lower limit of the k-th key, which leaves about
+// k + 2 candidates (their expected number, 32 (H(32) - H(32 - k)), is 9.1 for k = 8); these go
+// to a lane each and are ranked by counting.  Which of two experts is chosen is decided as in exact
+// arithmetic: where two keys that the choice depends on are nearer than fp32 can tell (a few tokens
+// in a thousand) the experts in question are ranked again in 64 bits.  Without a bias scores rise
+// with the logits, which are ranked themselves.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -20,7 +20,7 @@
 
 namespace mok {
 
-constexpr int kSelectWarps = 4;
+constexpr int kSelectWarps = 2;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxGroups = 32;
 
@@ -35,7 +35,6 @@ struct SelectParams {
   int groups, kept, n;     // groups, how many stay, experts of one
   int lanes, log_lanes;    // of a group: a power of two
   int chunk;               // experts of a lane
-  int sets;                // a power of two, at least k
   int top2, renorm;
   float scale;
 };
@@ -209,12 +208,13 @@ __device__ __noinline__ bool exact_groups(SelectRow<SOFTMAX, BIAS> r, const Sele
   return rank < p.kept;
 }
 
-// Bound by issue: at T = 16384, E = 384, k = 8 with sigmoid scores and a bias, 24.9 us
-// (14.9 without a bias; 870 instructions per warp at 59% of the issue slots); ranking by rounds of a
-// maximum over the warp 47 us.
+// Bound by issue and its latencies: at T = 16384, E = 384, k = 8 with sigmoid scores and a bias 20.0 us
+// (13.9 without a bias; 4 at the copy rate), E = 256 with 4 of 8 groups 19.7.  All but 18 of a
+// token's instructions per expert and lane are the same for every E (670 per warp), and 2 tokens in
+// a warp share them but wait longer: 27 us.  Ranking by rounds of a maximum over the warp 47 us.
 // V: experts of a lane at most.  VEC: groups and runs are whole vectors of four.
 template <int V, bool VEC, bool SOFTMAX, bool BIAS>
-__global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 14 : 8) select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ __align__(16) float s_keys[kSelectWarps][kMaxE];
   __shared__ int s_list[kSelectWarps][kMaxE];
   __shared__ float s_key[kSelectWarps][kMaxK + 1];  // the chosen ones and the next, in order
@@ -312,18 +312,16 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_ker
     c[i] = i < own && stays ? r.key(c[i], b[i]) : kAbsent;
     best = fmaxf(best, c[i]);
   }
-  // The lower limit.  Lanes without experts would leave their set empty: the others are moved up first.
-  const int want = BIAS ? p.k + 1 : p.k;  // one more than k where the next one matters
-  const unsigned busy = __ballot_sync(kAll, best > kAbsent);
-  if (busy != kAll) {
-    if (best > kAbsent) keys[__popc(busy & ((1u << lane) - 1u))] = best;
-    __syncwarp();
-    best = lane < __popc(busy) ? keys[lane] : kAbsent;
-    __syncwarp();
+  // The `want`-th largest of the lanes' largest keys (one more than k where the next one matters).  (The
+  // least of the largest keys of 8 sets of lanes takes a tenth of the instructions and leaves 22
+  // candidates: 21.9 us in place of 20.0.)
+  const int want = BIAS ? p.k + 1 : p.k;
+  float limit = kAbsent;
+  for (int j = 0; j < want; ++j) {
+    limit = warp_top(best);
+    const unsigned at = __ballot_sync(kAll, best == limit);
+    if (lane == __ffs(at) - 1) best = kAbsent;
   }
-  float limit = best;
-  for (int o = 16; o >= p.sets; o >>= 1) limit = fmaxf(limit, __shfl_xor_sync(kAll, limit, o));
-  for (int o = p.sets >> 1; o; o >>= 1) limit = fminf(limit, __shfl_xor_sync(kAll, limit, o));
   // Candidates in ascending order: open experts with keys at the limit or above.  Beyond 32 of them, of
   // those at the limit only the first `want`, behind the others; fewer than k, shut off ones behind them.
   unsigned mine = 0;
@@ -382,8 +380,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 6 : 4) select_ker
   }
   __syncwarp();
   int idx = lane < min(want, n) ? s_idx[warp][lane] : 0;  // n >= k
-  // without a further candidate nothing that is not chosen exceeds the limit
-  const float key = lane < min(want, n) ? s_key[warp][lane] : lane == n ? limit : kAbsent;
+  const float key = lane < min(want, n) ? s_key[warp][lane] : kAbsent;
   if constexpr (BIAS) {
     // Neighbours in the order that are nearer than their errors, unless they are one and the same
     // number; such a pair at the border may have others as near behind it.
@@ -600,15 +597,12 @@ int mok_select_experts(const mok_dims* dims, const mok_selection* sel, const flo
   set_last_launches(0);
   if (dims->T == 0) return MOK_OK;
   SelectParams p{logits, sel_bias, topk_idx, topk_w, static_cast<int*>(ws), dims->T, dims->E, dims->k, sel->n_groups,
-                 sel->topk_groups, dims->E / sel->n_groups, 1, 0, 0, 1,
+                 sel->topk_groups, dims->E / sel->n_groups, 1, 0, 0,
                  sel->group_score == MOK_GROUP_TOP2, sel->renormalise != 0, sel->scale};
   while (2 * p.lanes * p.groups <= 32) {
     p.lanes *= 2;
     ++p.log_lanes;
   }
-  // one set more than k, so that the next key is mostly among the candidates; for k = 8 it is with 8 sets
-  // too, but for one token in 400 (8! / 8^8)
-  while (p.sets < std::min(dims->k + (sel_bias ? 1 : 0), 8)) p.sets *= 2;
   p.chunk = (p.n + p.lanes - 1) / p.lanes;  // at most 30: E <= 512
   const bool vec = p.n % 4 == 0;
   if (vec) p.chunk = (p.chunk + 3) / 4 * 4;
