@@ -456,12 +456,15 @@ struct SelectBwdParams {
 constexpr int kSelectBwdWarps = 8;
 
 // A warp takes a token: lane j < k the j-th chosen expert, whose gradient goes to its place of a
-// row of zeros in shared memory; then every lane writes vectors of four.  With p_j = s_j / sum s_i
+// row of zeros in shared memory; then every lane writes its up to four vectors of four.  With p_j = s_j / sum s_i
 //   renormalised: dl_j = scale p_j (dw_j - sum p_i dw_i) (times 1 - s_j for sigmoid scores);
 //   sigmoid:      dl_j = scale s_j (1 - s_j) dw_j;
-//   softmax:      dl_e = scale s_e (dw of e - sum s_i dw_i), for every expert.
+//   softmax:      dl_e = scale s_e (dw of e - sum s_i dw_i), for every expert (DENSE).
+// Bound by latency: the index, then its logit.  What does not depend on them is under way before.
+template <bool DENSE>
 __global__ void __launch_bounds__(32 * kSelectBwdWarps) select_bwd_kernel(const __grid_constant__ SelectBwdParams p) {
   __shared__ float4 s_up[kSelectBwdWarps][kMaxE / 4];
+  constexpr int kVec = kMaxE / 128;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* up = reinterpret_cast<float*>(s_up[warp]);
   const int nvec = p.E / 4;
@@ -475,12 +478,6 @@ __global__ void __launch_bounds__(32 * kSelectBwdWarps) select_bwd_kernel(const 
     if (lane < p.k) {
       const int64_t r = t * p.k + lane;
       e = p.topk_idx[r];
-      if (e < 0 || e >= p.E) {
-        record_status(p.status, MOK_ERR_DEVICE_CHECK);
-        e = -1;
-      } else {
-        l = row[e];
-      }
       if (p.dw) {
         dw = p.dw[r];
       } else {
@@ -489,24 +486,33 @@ __global__ void __launch_bounds__(32 * kSelectBwdWarps) select_bwd_kernel(const 
           for (int n = 0; n < p.ldp; ++n) dw += p.partial[(int64_t)pos * p.ldp + n];
       }
     }
-    const bool on = l > kShutOff;  // not NaN either
-    const bool dense = p.softmax && !p.renorm;
-    float top = -INFINITY, sum = 1.0f;
-    if (dense) {
-      for (int v = lane; v < nvec; v += 32) {
-        const float4 q = reinterpret_cast<const float4*>(row)[v];
-        top = fmaxf(fmaxf(fmaxf(top, q.x), fmaxf(q.y, q.z)), q.w);  // fmaxf passes NaN by
+    float4 x[kVec], q[DENSE ? kVec : 1];  // aux; logits
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int v = lane + 32 * i;
+      x[i] = p.aux && v < nvec ? reinterpret_cast<const float4*>(p.aux + t * p.E)[v] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if constexpr (DENSE)
+        q[i] = v < nvec ? reinterpret_cast<const float4*>(row)[v] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+    if (lane < p.k) {
+      if (e < 0 || e >= p.E) {
+        record_status(p.status, MOK_ERR_DEVICE_CHECK);
+        e = -1;
+      } else {
+        l = row[e];
       }
+    }
+    const bool on = l > kShutOff;  // not NaN either
+    float top = -INFINITY, sum = 1.0f, g = 0.0f, inner = 0.0f;
+    if constexpr (DENSE) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) top = fmaxf(fmaxf(fmaxf(top, q[i].x), fmaxf(q[i].y, q[i].z)), q[i].w);  // fmaxf passes NaN by
       top = warp_max(top);
       sum = 0.0f;
-      for (int v = lane; v < nvec; v += 32) {
-        const float4 q = reinterpret_cast<const float4*>(row)[v];
-        for (float a : {q.x, q.y, q.z, q.w}) sum += a > kShutOff ? expf(below(a, top)) : 0.0f;
-      }
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        for (float a : {q[i].x, q[i].y, q[i].z, q[i].w}) sum += a > kShutOff ? expf(below(a, top)) : 0.0f;
       sum = warp_sum(sum);
-    }
-    float g = 0.0f, inner = 0.0f;
-    if (dense) {
       const float s = on ? expf(below(l, top)) / sum : 0.0f;
       inner = warp_sum(on ? s * dw : 0.0f);
       g = on ? dw : 0.0f;
@@ -529,20 +535,19 @@ __global__ void __launch_bounds__(32 * kSelectBwdWarps) select_bwd_kernel(const 
     }
     if (e >= 0) up[e] = total;
     __syncwarp();
-    const int end = p.dl ? p.ldl / 4 : nvec;
-    for (int v = lane; v < end; v += 32) {
+    const int end = p.dl ? p.ldl / 4 : nvec;  // at most 128
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int v = lane + 32 * i;
+      if (v >= end) break;
       float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (v < nvec) {
         a = s_up[warp][v];
-        if (dense) {
-          const float4 q = reinterpret_cast<const float4*>(row)[v];
-          auto grad = [&](float x, float d) { return x > kShutOff ? p.scale * (expf(below(x, top)) / sum) * (d - inner) : 0.0f; };
-          a = make_float4(grad(q.x, a.x), grad(q.y, a.y), grad(q.z, a.z), grad(q.w, a.w));
+        if constexpr (DENSE) {
+          auto grad = [&](float l, float d) { return l > kShutOff ? p.scale * (expf(below(l, top)) / sum) * (d - inner) : 0.0f; };
+          a = make_float4(grad(q[i].x, a.x), grad(q[i].y, a.y), grad(q[i].z, a.z), grad(q[i].w, a.w));
         }
-        if (p.aux) {
-          const float4 x = reinterpret_cast<const float4*>(p.aux + t * p.E)[v];
-          a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-        }
+        a.x += x[i].x; a.y += x[i].y; a.z += x[i].z; a.w += x[i].w;
         reinterpret_cast<float4*>(p.dlogits + t * p.E)[v] = a;
       }
       if (p.dl) reinterpret_cast<uint2*>(p.dl + t * p.ldl)[v] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
@@ -573,7 +578,8 @@ cudaError_t launch_select_backward(const mok_dims* dims, const mok_selection* se
                     sel->renormalise != 0, sel->scale};
   const int64_t blocks = (dims->T + kSelectBwdWarps - 1) / kSelectBwdWarps;
   prof_begin("select_bwd", s);
-  select_bwd_kernel<<<(int)std::min<int64_t>(blocks, (int64_t)num_sms() * 8), 32 * kSelectBwdWarps, 0, s>>>(p);
+  auto k = p.softmax && !p.renorm ? select_bwd_kernel<true> : select_bwd_kernel<false>;
+  k<<<(int)std::min<int64_t>(blocks, (int64_t)num_sms() * 8), 32 * kSelectBwdWarps, 0, s>>>(p);
   prof_end(s);
   return cudaGetLastError();
 }
