@@ -167,7 +167,8 @@ int mok_mx_quantize_rows(int64_t rows, int K, const void *src, void *q, void *sc
  * section "Chồng lấp tính toán và truyền tải trong MoE".
  *   x[T,d] bf16, W_router[d,E] bf16, bias[E] fp32 or NULL
  *   -> topk_idx[T,k] int32 (slot order = descending logit), topk_w[T,k] fp32,
- *      logits[T,E] fp32 (optional, NULL to skip). */
+ *      logits[T,E] fp32 (optional, NULL to skip).
+ * topk_idx and topk_w may both be NULL: logits alone, for mok_select_experts. */
 int mok_route(const mok_dims *dims, const void *x, const void *W_router, const float *bias,
               int32_t *topk_idx, float *topk_w, float *logits, void *ws, size_t ws_bytes,
               mok_stream_t stream);

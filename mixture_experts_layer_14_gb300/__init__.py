@@ -8,7 +8,9 @@ kernels.  There is no fallback: without the compiled library every call raises.
 Entry points mirror the C ABI: :func:`route`, :func:`dispatch_index`, :func:`moe_forward`,
 :func:`moe_backward`, :func:`layer_forward_host`, plus :class:`MoELayer`, a small convenience
 holder of weights and workspaces.  Around the layer: :func:`rms_norm`, :func:`balance_loss`,
-:func:`grad_norm` and :class:`AdamW`, and :class:`MoEBlock`, which runs them together.
+:func:`grad_norm` and :class:`AdamW`, and :class:`MoEBlock`, which runs them together.  Other routers:
+:func:`select_experts`; norms on both sides of a branch: :func:`sandwich_norm`; activations kept in
+8 bits: :func:`activation_pack`, :func:`saved_pack`.
 """
 
 import ctypes
@@ -320,16 +322,17 @@ def _weights_struct(D, W):
         W["prepared_bwd"].data_ptr() if W.get("prepared_bwd") is not None else None)
 
 
-def route(D, x, W_router, bias, ws, want_logits=False):
-    """Returns (topk_idx[T,k] int32, topk_w[T,k] fp32, logits[T,E] fp32 or None)."""
+def route(D, x, W_router, bias, ws, want_logits=False, want_topk=True):
+    """Returns (topk_idx[T,k] int32, topk_w[T,k] fp32, logits[T,E] fp32 or None); with
+    want_topk=False the logits alone (None, None, logits), for :func:`select_experts`."""
     dev = x.device
     _want(x, "x", (D.T, D.d), torch.bfloat16, dev)
     _want(W_router, "W_router", (D.d, D.E), torch.bfloat16, dev)
     if bias is not None:
         _want(bias, "bias", (D.E,), torch.float32, dev)
-    idx = torch.empty((D.T, D.k), dtype=torch.int32, device=dev)
-    w = torch.empty((D.T, D.k), dtype=torch.float32, device=dev)
-    logits = torch.empty((D.T, D.E), dtype=torch.float32, device=dev) if want_logits else None
+    idx = torch.empty((D.T, D.k), dtype=torch.int32, device=dev) if want_topk else None
+    w = torch.empty((D.T, D.k), dtype=torch.float32, device=dev) if want_topk else None
+    logits = torch.empty((D.T, D.E), dtype=torch.float32, device=dev) if want_logits or not want_topk else None
     _check(lib().mok_route(ctypes.byref(D), _ptr(x), _ptr(W_router), _ptr(bias), _ptr(idx), _ptr(w),
                            _ptr(logits), _ptr(ws), ws.numel(), _stream()))
     return idx, w, logits
@@ -874,8 +877,8 @@ class MoELayer:
         self._ws_bwd = None
 
     def forward(self, x, training=False, x_mx=None, want_logits=False):
-        idx, w, self.logits = route(self.D, x, self.W["W_router"], self.W.get("bias"), self.ws,
-                                    want_logits or self.selection is not None)
+        idx, w, self.logits = route(self.D, x, self.W["W_router"], self.W.get("bias"), self.ws, want_logits,
+                                    want_topk=self.selection is None)
         n = last_launch_count()
         if self.selection is not None:
             idx, w = select_experts(self.D, self.selection, self.logits, self.ws, bias=self.W.get("balance_bias"))

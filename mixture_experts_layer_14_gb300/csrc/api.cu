@@ -746,7 +746,8 @@ int mok_route(const mok_dims* dims, const void* x, const void* W_router, const f
               mok_stream_t stream) {
   int rc = check_dims(dims);
   if (rc != MOK_OK) return rc;
-  if (!ws || (dims->T > 0 && (!x || !W_router || !topk_idx || !topk_w))) return MOK_ERR_INVALID_ARG;
+  if (!ws || (dims->T > 0 && (!x || !W_router || (topk_idx != nullptr) != (topk_w != nullptr) || (!topk_idx && !logits))))
+    return MOK_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(W_router) || !aligned16(ws)) return MOK_ERR_UNSUPPORTED;
   if (ws_bytes < layout_fwd(dims).total) return MOK_ERR_WORKSPACE;
   g_last_launches = 0;

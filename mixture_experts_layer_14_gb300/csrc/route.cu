@@ -45,6 +45,7 @@ __device__ __forceinline__ void topk_insert(float (&tv)[kMaxK], int (&ti)[kMaxK]
 // w_j = softmax(l)[e_j] / sum_sel softmax(l)[e_i] = exp(l_j - l_0) / sum_i exp(l_i - l_0)
 __device__ __forceinline__ void write_route(const RouteParams& p, int t, const float (&tv)[kMaxK],
                                             const int (&ti)[kMaxK]) {
+  if (!p.topk_idx) return;  // logits alone
   float ex[kMaxK];
   float den = 0.0f;
 #pragma unroll

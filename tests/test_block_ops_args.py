@@ -75,6 +75,15 @@ def test_moe_backward_select():
     assert call(_sel(), P) == INVALID  # W is empty
 
 
+def test_route_for_logits_alone():
+    D = mok.dims(16, 128, 16, 4, 128, 0, 0)
+
+    def call(idx, w, logits, n=16):
+        return ensure_lib().mok_route(ctypes.byref(D), P, P, NULL, idx, w, logits, P, n, NULL)
+    assert call(NULL, NULL, NULL) == INVALID and call(P, NULL, P) == INVALID and call(NULL, P, P) == INVALID
+    assert call(NULL, NULL, P) == WORKSPACE  # as far as the size of the workspace
+
+
 def test_selection_binding():
     for bad in (dict(scoring="relu"), dict(group_score="sum")):
         with pytest.raises(ValueError):

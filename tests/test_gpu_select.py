@@ -250,3 +250,21 @@ def test_layer_with_a_selection(scoring, renorm, dtype):
         assert_close(k, f64(g["d" + k]), f64(grads[k]))
     plain = _block.select_grad(logits, ref, f64(grads["w"]), scoring, renorm, 2.5)
     assert_close("dlogits from dw", plain, f64(grads["dl"]), 1e-3, 1e-3)
+
+
+def test_layer_with_experts_shut_off_by_the_routers_bias():
+    """Fewer open experts than k: weights 0 for the others and nothing to report."""
+    ensure_lib()
+    D = dims_of(LAYER)
+    W = to_dev(make_layer(LAYER, "cpu"))
+    x = W.pop("x")
+    W["bias"] = torch.full((16,), -float("inf"), device="cuda")
+    W["bias"][[3, 11]] = 0.5
+    layer = mok.MoELayer(D, W, selection=mok.Selection("sigmoid", scale=2.0))
+    y = layer.forward(x)
+    assert mok.read_status(layer.ws) == 0 and torch.isfinite(y).all()
+    idx, w = (layer.routing[k].cpu() for k in ("topk_idx", "topk_w"))
+    assert (idx[:, 2:] == torch.tensor([0, 1])).all() and (w[:, 2:] == 0).all()
+    assert (idx[:, :2].sort(1).values == torch.tensor([3, 11])).all() and np.abs(f64(w[:, :2].sum(1)) - 2.0).max() < 1e-5
+    logits = mok.route(D, x, W["W_router"], W["bias"], layer.ws, want_topk=False)
+    assert logits[:2] == (None, None) and torch.equal(logits[2], layer.logits)
