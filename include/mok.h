@@ -477,7 +477,8 @@ typedef struct {
  *      x_scales, h_codes, h_scales (all or none) what the backward pass reads in 8 bits: the MXFP8
  *      forms of x and of h (before its rounding to res_type), codes[T,d] and scales[T,d/32].
  * residual_out may be residual, y may be x.  T >= 0, 0 < d <= 32768, d % 8 == 0 (d % 128 == 0 with
- * codes of any kind); 16-byte aligned pointers (token_gate 4).  One launch. */
+ * codes of any kind); 16-byte aligned pointers (token_gate 4).  There is no status word: a row whose
+ * copy does not arrive within the library's limit on waits is NaN.  One launch. */
 int mok_sandwich_norm(const mok_sandwich *args, int64_t T, int d, const void *x,
                       const void *residual, void *residual_out, void *y, void *codes, void *scales,
                       int scale_layout, void *x_codes, void *x_scales, void *h_codes,
@@ -498,8 +499,8 @@ size_t mok_sandwich_norm_workspace_size(int64_t T, int d);
  *   wrote them: the gradients are then those at the values that these hold.
  *   -> dx[T,d] bf16, dresidual[T,d] of res_type, dpost_weight[d], dgate[d] (with gate),
  *      dtoken_gate[T] (with token_gate), dweight[d] (with weight) fp32.
- * dx may be dy, dresidual may be dres.  Sizes and alignment as in mok_sandwich_norm.  Two launches,
- * the second begins under the first. */
+ * dx may be dy, dresidual may be dres.  Sizes, alignment and waits as in mok_sandwich_norm.  Two
+ * launches, the second begins under the first. */
 int mok_sandwich_norm_backward(const mok_sandwich *args, int64_t T, int d, const void *dy,
                                const void *dres, const void *x, const void *x_scales, const void *h,
                                const void *h_scales, void *dx, void *dresidual, float *dpost_weight,

@@ -863,6 +863,8 @@ class MoELayer:
     def __init__(self, D, W, device=None, selection=None, checkpoint=None, saved=None):
         if checkpoint not in (None, "mxfp8"):
             raise ValueError("checkpoint must be None or 'mxfp8'")
+        if saved is not None and checkpoint is None:
+            raise ValueError("saved needs checkpoint (without one it holds the layer's activations until backward)")
         if saved is not None:
             _want(saved, "saved", (saved_size(D),), torch.uint8, W["W_gate"].device)
         self.D = D

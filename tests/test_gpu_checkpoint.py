@@ -251,7 +251,9 @@ def test_block_refusals():
     ensure_lib()
     D, W, x, dY = _layer("bf16")
     W["norm"] = torch.ones(256, device="cuda")
-    for bad in (dict(res_scale=0.5), dict(checkpoint="int8"), dict(saved=torch.empty(8, dtype=torch.uint8, device="cuda"))):
+    small = torch.empty(8, dtype=torch.uint8, device="cuda")
+    whole = torch.empty(mok.saved_size(D), dtype=torch.uint8, device="cuda")
+    for bad in (dict(res_scale=0.5), dict(checkpoint="int8"), dict(saved=small, checkpoint="mxfp8"), dict(saved=whole)):
         with pytest.raises(ValueError):
             mok.MoEBlock(D, W, **bad)
     with pytest.raises(ValueError):

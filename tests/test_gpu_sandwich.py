@@ -120,6 +120,15 @@ def test_codes_and_checkpoint(T, d, res, gate, mx, want_y):
         assert (s.astype(np.int64) - 127 == want)[clear | (amax == 0)].all(), name
 
 
+def test_checkpoint_without_a_next_norm():
+    ensure_lib()
+    t = _dev(_make(70, 384, "bf16", "f32", "both", 4))
+    args = dict(gate=t["gate"], token_gate=t["token_gate"], res_scale=A)
+    full = mok.sandwich_norm(t["x"], t["r"], t["post"], weight=t["weight"], save="mxfp8", **args)
+    last = mok.sandwich_norm(t["x"], t["r"], t["post"], save="mxfp8", **args)
+    assert set(last) == set(full) - {"y"} and all(torch.equal(last[k], full[k]) for k in last)
+
+
 @pytest.mark.parametrize("T,d,res,w,gate", CASES)
 @pytest.mark.parametrize("next_norm,dh,packed", [(True, True, False), (True, False, False), (False, True, False),
                                                  (True, True, True), (False, True, True)])
