@@ -200,11 +200,14 @@ def _stream():
     return torch.cuda.current_stream().cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream_of(dev):
     """The current stream of the tensors' device, which has to be the current one."""
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _current_device():
         raise ValueError(f"the tensors live on {dev}, not on the current device cuda:{torch.cuda.current_device()}")
-    return _stream()
+    return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _want(t, name, shape, dtype, device, check_device=True):
@@ -397,9 +400,10 @@ _ELEM = {torch.bfloat16: 0, torch.float32: 1}   # mok_elem
 
 
 def _elem(t, name):
-    if t.dtype not in _ELEM:
+    kind = _ELEM.get(t.dtype)
+    if kind is None:
         raise ValueError(f"{name}: dtype {t.dtype} is neither bfloat16 nor float32")
-    return _ELEM[t.dtype]
+    return kind
 
 
 def _scale_bytes(rows, K, layout):
@@ -485,9 +489,10 @@ def rms_norm_backward(dy, s, weight, eps=1e-6, dres=None, ws=None):
 def _sandwich(shape, dev, kind, post_weight, weight, gate, token_gate, res_scale, eps):
     T, d = shape
     _want(post_weight, "post_weight", (d,), post_weight.dtype, dev)
-    for t, name in ((weight, "weight"), (gate, "gate")):
-        if t is not None:
-            _want(t, name, (d,), t.dtype, dev)
+    if weight is not None:
+        _want(weight, "weight", (d,), weight.dtype, dev)
+    if gate is not None:
+        _want(gate, "gate", (d,), gate.dtype, dev)
     if token_gate is not None:
         _want(token_gate, "token_gate", (T,), torch.float32, dev)
     return Sandwich(eps, res_scale, kind, _elem(post_weight, "post_weight"), 0 if gate is None else _elem(gate, "gate"),
@@ -517,22 +522,22 @@ def sandwich_norm(x, residual, post_weight, weight=None, gate=None, token_gate=N
         raise ValueError("mx must be None, 'rows' or 'atoms', save None or 'mxfp8'")
     if mx is not None and weight is None:
         raise ValueError("mx needs weight")
-    out = {"residual": torch.empty_like(residual)}
+    h = torch.empty_like(residual)
+    out = {"residual": h}
+    y = codes = scales = xc = xs = hc = hs = None
     if weight is not None and want_y:
-        out["y"] = torch.empty_like(x)
+        y = out["y"] = torch.empty_like(x)
     if mx is not None:
-        out["codes"] = torch.empty(shape, dtype=torch.uint8, device=dev)
-        out["scales"] = torch.empty((T, d // 32) if mx == "rows" else (_scale_bytes(T, d, mx),), dtype=torch.uint8,
-                                    device=dev)
+        codes = out["codes"] = torch.empty(shape, dtype=torch.uint8, device=dev)
+        scales = out["scales"] = torch.empty((T, d // 32) if mx == "rows" else (_scale_bytes(T, d, mx),),
+                                             dtype=torch.uint8, device=dev)
     if save is not None:
-        for k in ("x", "h"):
-            out[k + "_codes"] = torch.empty(shape, dtype=torch.uint8, device=dev)
-            out[k + "_scales"] = torch.empty((T, d // 32), dtype=torch.uint8, device=dev)
-    get = out.get
+        xc, hc = (torch.empty(shape, dtype=torch.uint8, device=dev) for _ in range(2))
+        xs, hs = (torch.empty((T, d // 32), dtype=torch.uint8, device=dev) for _ in range(2))
+        out["x_codes"], out["x_scales"], out["h_codes"], out["h_scales"] = xc, xs, hc, hs
     _check(lib().mok_sandwich_norm(
-        ctypes.byref(a), T, d, x.data_ptr(), residual.data_ptr(), out["residual"].data_ptr(), _ptr(get("y")),
-        _ptr(get("codes")), _ptr(get("scales")), 1 if mx == "atoms" else 0, _ptr(get("x_codes")), _ptr(get("x_scales")),
-        _ptr(get("h_codes")), _ptr(get("h_scales")), _stream_of(dev)))
+        ctypes.byref(a), T, d, x.data_ptr(), residual.data_ptr(), h.data_ptr(), _ptr(y), _ptr(codes), _ptr(scales),
+        1 if mx == "atoms" else 0, _ptr(xc), _ptr(xs), _ptr(hc), _ptr(hs), _stream_of(dev)))
     return out
 
 
@@ -585,17 +590,24 @@ def sandwich_norm_backward(x, h, post_weight, dy=None, dres=None, weight=None, g
     if ws is None:
         ws = torch.empty(sandwich_norm_workspace_size(T, d), dtype=torch.uint8, device=dev)
     _want_ws(ws, dev)
-    out = {"dx": torch.empty(shape, dtype=torch.bfloat16, device=dev),
-           "dresidual": torch.empty(shape, dtype=kind, device=dev),
-           "dpost_weight": torch.empty((d,), dtype=torch.float32, device=dev)}
-    for t, name, n in ((weight, "dweight", d), (gate, "dgate", d), (token_gate, "dtoken_gate", T)):
-        if t is not None:
-            out[name] = torch.empty((n,), dtype=torch.float32, device=dev)
-    get = out.get
+    f32 = torch.float32
+    dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    dresidual = torch.empty(shape, dtype=kind, device=dev)
+    dpost = torch.empty((d,), dtype=f32, device=dev)
+    dweight = torch.empty((d,), dtype=f32, device=dev) if weight is not None else None
+    dgate = torch.empty((d,), dtype=f32, device=dev) if gate is not None else None
+    dtoken = torch.empty((T,), dtype=f32, device=dev) if token_gate is not None else None
     _check(lib().mok_sandwich_norm_backward(
         ctypes.byref(a), T, d, _ptr(dy), _ptr(dres), rows.data_ptr(), _ptr(x_scales), _ptr(h_rows), _ptr(h_scales),
-        out["dx"].data_ptr(), out["dresidual"].data_ptr(), out["dpost_weight"].data_ptr(), _ptr(get("dgate")),
-        _ptr(get("dtoken_gate")), _ptr(get("dweight")), ws.data_ptr(), ws.numel(), _stream_of(dev)))
+        dx.data_ptr(), dresidual.data_ptr(), dpost.data_ptr(), _ptr(dgate), _ptr(dtoken), _ptr(dweight), ws.data_ptr(),
+        ws.numel(), _stream_of(dev)))
+    out = {"dx": dx, "dresidual": dresidual, "dpost_weight": dpost}
+    if weight is not None:
+        out["dweight"] = dweight
+    if gate is not None:
+        out["dgate"] = dgate
+    if token_gate is not None:
+        out["dtoken_gate"] = dtoken
     return out
 
 
