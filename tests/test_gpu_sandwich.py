@@ -58,11 +58,14 @@ def _packed(t):
             q.double().numpy() * np.repeat(2.0 ** s, 32, axis=-1))
 
 
-CASES = [(311, 8192, "bf16", "bf16", "channel"), (5, 8448, "f32", "f32", "both"), (1, 8, "bf16", "bf16", "none"), (1, 7168, "bf16", "bf16", "none"), (3, 256, "f32", "bf16", "both"),
+CASES = [(1, 8, "bf16", "bf16", "none"), (1, 7168, "bf16", "bf16", "none"), (3, 256, "f32", "bf16", "both"),
          (9, 264, "bf16", "f32", "channel"), (700, 64, "bf16", "bf16", "token"), (517, 1544, "f32", "f32", "both"),
          (400, 4096, "bf16", "bf16", "channel"), (330, 7168, "f32", "bf16", "token"), (7, 8200, "bf16", "f32", "both"),
          (310, 16384, "bf16", "bf16", "none"), (5, 16392, "f32", "f32", "both"), (157, 32768, "bf16", "bf16", "token"),
-         (2500, 128, "f32", "bf16", "none")]
+         (2500, 128, "f32", "bf16", "none"), (311, 8192, "bf16", "bf16", "channel"), (5, 8448, "f32", "f32", "both"),
+         # many rows per block, several times around the ring
+         (1300, 4096, "f32", "bf16", "both"), (2500, 2056, "bf16", "f32", "channel"), (9001, 512, "bf16", "bf16", "token"),
+         (20011, 128, "f32", "bf16", "none"), (1100, 7168, "f32", "bf16", "none"), (1500, 8192, "bf16", "bf16", "both")]
 
 
 @pytest.mark.parametrize("T,d,res,w,gate", CASES)
