@@ -51,6 +51,12 @@ __device__ __forceinline__ float warp_top(float v) {  // not NaN
   return r;
 }
 
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // l - top for the exponent: 0 for the largest, whatever it is.
 template <class F>
 __device__ __forceinline__ F below(F l, F top) { return l == top ? F(0) : l - top; }
@@ -208,10 +214,10 @@ __device__ __noinline__ bool exact_groups(SelectRow<SOFTMAX, BIAS> r, const Sele
   return rank < p.kept;
 }
 
-// Bound by issue and its latencies: at T = 16384, E = 384, k = 8 with sigmoid scores and a bias 20.0 us
-// (13.9 without a bias; 4 at the copy rate), E = 256 with 4 of 8 groups 19.7.  All but 18 of a
-// token's instructions per expert and lane are the same for every E (670 per warp), and 2 tokens in
-// a warp share them but wait longer: 27 us.  Ranking by rounds of a maximum over the warp 47 us.
+// Bound by issue and its latencies: at T = 16384, E = 384, k = 8 with sigmoid scores and a bias 18.5 us
+// (12.2 without a bias; 4 at the copy rate), E = 256 with 4 of 8 groups 18.6.  Most of a token's
+// instructions do not depend on E, and 2 tokens in a warp share them but wait longer: 27 us where one
+// took 23.6.  Ranking by rounds of a maximum over the warp 47 us.
 // V: experts of a lane at most.  VEC: groups and runs are whole vectors of four.
 template <int V, bool VEC, bool SOFTMAX, bool BIAS>
 __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 14 : 8) select_kernel(const __grid_constant__ SelectParams p) {
@@ -252,12 +258,14 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 14 : 8) select_ke
       }
     }
   }
-  bool bad = false;
   float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bad |= c[i] != c[i];
-    top = fmaxf(top, c[i]);  // passes NaN by
+  for (int i = 0; i < V; ++i) top = max_or_nan(top, c[i]);
+  bool bad = top != top;
+  if (bad) {
+    top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmaxf(top, c[i]);  // passes NaN by
   }
   if (BIAS && t == 0) {  // the same for every token
 #pragma unroll
@@ -307,26 +315,29 @@ __global__ void __launch_bounds__(32 * kSelectWarps, V <= 16 ? 14 : 8) select_ke
     }
   }
   float best = kAbsent;
+  const int here = stays ? own : 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    c[i] = i < own && stays ? r.key(c[i], b[i]) : kAbsent;
+    c[i] = (VEC ? i / 4 * 4 : i) < here ? r.key(c[i], b[i]) : kAbsent;  // VEC: whole fours
     best = fmaxf(best, c[i]);
   }
   // The `want`-th largest of the lanes' largest keys (one more than k where the next one matters).  (The
   // least of the largest keys of 8 sets of lanes takes a tenth of the instructions and leaves 22
-  // candidates: 21.9 us in place of 20.0.)
+  // candidates: 21.9 us where this took 20.0.)
   const int want = BIAS ? p.k + 1 : p.k;
-  float limit = kAbsent;
+  float limit = kAbsent, left = best;
   for (int j = 0; j < want; ++j) {
-    limit = warp_top(best);
-    const unsigned at = __ballot_sync(kAll, best == limit);
-    if (lane == __ffs(at) - 1) best = kAbsent;
+    limit = warp_top(left);
+    if (left == limit) left = kAbsent;  // equal ones together: the limit is then lower than it might be
   }
+  if (limit == kAbsent && __popc(__ballot_sync(kAll, best > kAbsent)) >= want)  // or all of them: the least of the lanes' largest
+    limit = -warp_top(best > kAbsent ? -best : kAbsent);
   // Candidates in ascending order: open experts with keys at the limit or above.  Beyond 32 of them, of
   // those at the limit only the first `want`, behind the others; fewer than k, shut off ones behind them.
   unsigned mine = 0;
+  const float from = fmaxf(limit, kMasked / 2);  // below every open key
 #pragma unroll
-  for (int i = 0; i < V; ++i) mine |= (c[i] >= limit && c[i] > kMasked ? 1u : 0u) << i;
+  for (int i = 0; i < V; ++i) mine |= (c[i] >= from ? 1u : 0u) << i;
   auto scan = [&](unsigned v) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
