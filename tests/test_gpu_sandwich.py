@@ -243,3 +243,34 @@ def test_rows_that_are_not_finite_stay_their_own():
     a = mok.sandwich_norm_backward(v["x"], clean["residual"], v["post"], dy=dy, weight=v["weight"])
     b = mok.sandwich_norm_backward(x, out["residual"], v["post"], dy=dy, weight=v["weight"])
     assert torch.equal(a["dx"][ok], b["dx"][ok]) and torch.equal(a["dresidual"][ok], b["dresidual"][ok])
+
+
+def test_more_than_2_31_elements():
+    """The last rows of a tensor whose offsets pass 32 bits, against the same rows by themselves."""
+    ensure_lib()
+    T, d, n = 262400, 8192, 5
+    post, w = torch.linspace(0.5, 1.5, d, device="cuda"), torch.linspace(1.5, 0.5, d, device="cuda")
+    x = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+    r = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for t in (x, r):
+        t[-n:] = torch.randn((n, d), generator=g, device="cuda").bfloat16()
+    out = mok.sandwich_norm(x, r, post, weight=w, save="mxfp8")
+    few = mok.sandwich_norm(x[-n:].clone(), r[-n:].clone(), post, weight=w, save="mxfp8")
+    assert all(torch.equal(out[k][-n:], few[k]) and not out[k][:1].float().any() for k in ("residual", "y", "x_codes", "h_codes"))
+    assert all(torch.equal(out[k][-n:], few[k]) for k in ("x_scales", "h_scales"))
+    x8, h8 = ((out[k + "_codes"], out[k + "_scales"]) for k in ("x", "h"))
+    few8 = [tuple(t[-n:].clone() for t in p) for p in (x8, h8)]
+    del r, out["y"], out["residual"]
+    dy = x  # the gradient of the last rows, zero elsewhere
+    for a, b in ((x8, h8), few8):
+        m = len(a[0])
+        got = mok.sandwich_norm_backward(a, b, post, dy=dy[-m:] if m == T else dy[-n:].clone(), weight=w)
+        if m == T:
+            tail = {k: v[-n:].clone() if v.dim() == 2 else v for k, v in got.items()}
+            assert not got["dx"][:1000].any()
+            del got
+    assert torch.equal(tail["dx"], got["dx"]) and torch.equal(tail["dresidual"], got["dresidual"])
+    for k in ("dpost_weight", "dweight"):  # the same rows in another order of blocks
+        size = got[k].abs().max()
+        assert ((tail[k] - got[k]).abs() <= 2.0 ** -18 * size).all(), k

@@ -268,3 +268,21 @@ def test_layer_with_experts_shut_off_by_the_routers_bias():
     assert (idx[:, :2].sort(1).values == torch.tensor([3, 11])).all() and np.abs(f64(w[:, :2].sum(1)) - 2.0).max() < 1e-5
     logits = mok.route(D, x, W["W_router"], W["bias"], layer.ws, want_topk=False)
     assert logits[:2] == (None, None) and torch.equal(logits[2], layer.logits)
+
+
+def test_more_than_2_31_logits():
+    ensure_lib()
+    T, E, n = 5600000, 384, 7
+    l = torch.zeros((T, E), device="cuda")
+    l[-n:] = torch.randn((n, E), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    D, few, sel = mok.dims(T, 128, E, 8, 128, 0, 0), mok.dims(n, 128, E, 8, 128, 0, 0), mok.Selection("sigmoid", scale=2.0)
+    ws, b = _ws(), torch.zeros(E, device="cuda")
+    idx, w = mok.select_experts(D, sel, l, ws, bias=b)
+    i, v = mok.select_experts(few, sel, l[-n:].clone(), ws, bias=b)
+    assert torch.equal(idx[-n:], i) and torch.equal(w[-n:], v) and (idx[:1000].cpu() == torch.arange(8)).all()
+    dw = torch.zeros((T, 8), device="cuda")
+    dw[-n:] = 1.0
+    dw[-n:, 0] = 3.0
+    dl = mok.select_experts_backward(D, sel, l, idx, dw, ws)
+    assert torch.equal(dl[-n:], mok.select_experts_backward(few, sel, l[-n:].clone(), i, dw[-n:].clone(), ws))
+    assert not dl[:1000].any() and mok.read_status(ws) == 0
