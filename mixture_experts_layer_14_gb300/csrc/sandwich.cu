@@ -118,7 +118,7 @@ __device__ __forceinline__ Pairs row_pairs(uint32_t at, int v) {  // vector v of
 // rate, 587 instructions per warp and row; with rows by asynchronous copies of the threads' own vectors
 // 234 us and 668, with scalar arithmetic and sums in every lane besides 257 and 845.
 template <int V, bool F32, bool RING, int MT>
-__global__ void __launch_bounds__(MT, V == 1 ? 2 : 1) sandwich_kernel(const __grid_constant__ SandwichParams p) {
+__global__ void __launch_bounds__(MT, V == 1 || MT <= 320 ? 2 : 1) sandwich_kernel(const __grid_constant__ SandwichParams p) {
   __shared__ float smem[2][2][16];
   __shared__ __align__(8) uint64_t bars[8][3];
   __shared__ int s_abort;
@@ -647,18 +647,19 @@ struct SandwichShape {
   int v, threads, rows, blocks;
 };
 constexpr int kSmemPerSm = 227 * 1024;  // for the blocks of an SM together
-constexpr int kSmemOwn = 3072;          // of a block: reserved and static
+constexpr int kSmemOwn = 3 * 1024;      // of a block: reserved and static
 constexpr int kPlainSmem = 40 * 1024;   // dynamic bytes that need no attribute
 constexpr int kWideThreads = 512;       // of a block with two vectors per thread and more: 128 registers each
 // Forward: one vector per thread up to 512 threads, of which 1024 fit an SM (64 registers): 2^25 elements
-// with a bf16 residual at d = 4096 in 45 us, 61 with one block per SM, 40 at the copy rate.
+// with a bf16 residual at d = 4096 in 45 us, 61 with one block per SM, 40 at the copy rate.  With two
+// vectors two blocks fit up to 320 threads (96 registers): T = 8192, d = 5120 58 us, 61 with one.
 static SandwichShape sandwich_shape(int d) {
   SandwichShape n;
   const int nvec = d / 8;
   n.v = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8;
   n.threads = ((nvec + n.v - 1) / n.v + 31) / 32 * 32;
   n.rows = n.threads == 32 ? 8 : 1;
-  n.blocks = n.v == 1 ? std::max(1, std::min(1024 / (n.threads * n.rows), 8)) : 1;
+  n.blocks = n.v == 1 ? std::max(1, std::min(1024 / (n.threads * n.rows), 8)) : n.v == 2 && n.threads <= 320 ? 2 : 1;
   return n;
 }
 // Backward: one warp more fetches (not for the widest rows, which have no ring).  A vector of a thread
@@ -738,7 +739,7 @@ int mok_sandwich_norm(const mok_sandwich* a, int64_t T, int d, const void* x, co
   void (*k)(const SandwichParams) = nullptr;
   auto pick = [&](auto type, auto ring) {
     constexpr bool F = decltype(type)::value, R = decltype(ring)::value;
-    k = n.v == 1 ? sandwich_kernel<1, F, R, 512> : n.v == 2 ? sandwich_kernel<2, F, R, 512>
+    k = n.v == 1 ? sandwich_kernel<1, F, R, 512> : n.v == 2 ? (n.threads <= 320 ? sandwich_kernel<2, F, R, 320> : sandwich_kernel<2, F, R, 512>)
         : n.v == 4 ? sandwich_kernel<4, F, R, 512> : sandwich_kernel<8, F, false, 512>;
   };
   if (f32 && p.depth) pick(std::true_type{}, std::true_type{});

@@ -65,7 +65,8 @@ CASES = [(1, 8, "bf16", "bf16", "none"), (1, 7168, "bf16", "bf16", "none"), (3, 
          (2500, 128, "f32", "bf16", "none"), (311, 8192, "bf16", "bf16", "channel"), (5, 8448, "f32", "f32", "both"),
          # many rows per block, several times around the ring
          (1300, 4096, "f32", "bf16", "both"), (2500, 2056, "bf16", "f32", "channel"), (9001, 512, "bf16", "bf16", "token"),
-         (20011, 128, "f32", "bf16", "none"), (1100, 7168, "f32", "bf16", "none"), (1500, 8192, "bf16", "bf16", "both")]
+         (20011, 128, "f32", "bf16", "none"), (1100, 7168, "f32", "bf16", "none"), (1500, 8192, "bf16", "bf16", "both"),
+         (1300, 5120, "bf16", "f32", "both"), (1301, 4360, "f32", "bf16", "channel")]
 
 
 @pytest.mark.parametrize("T,d,res,w,gate", CASES)
@@ -88,7 +89,7 @@ def test_forward(T, d, res, w, gate, next_norm):
 
 @pytest.mark.parametrize("T,d,res,gate,mx,want_y", [
     (1, 128, "bf16", "none", "rows", True), (130, 256, "f32", "both", "atoms", True), (33, 384, "bf16", "channel", "atoms", False),
-    (301, 7168, "bf16", "token", "rows", False), (3, 16512, "f32", "none", "atoms", True)])
+    (301, 7168, "bf16", "token", "rows", False), (1301, 5120, "f32", "both", "rows", True), (3, 16512, "f32", "none", "atoms", True)])
 def test_codes_and_checkpoint(T, d, res, gate, mx, want_y):
     """The MXFP8 output and the 8-bit forms of x and h: x's exactly; the others within half a step of
     their code (2^-4 of the value, 2^-10 of the scale below the smallest normal), and fp32 roundings
