@@ -478,7 +478,8 @@ typedef struct {
  *      forms of x and of h (before its rounding to res_type), codes[T,d] and scales[T,d/32].
  * residual_out may be residual, y may be x.  T >= 0, 0 < d <= 32768, d % 8 == 0 (d % 128 == 0 with
  * codes of any kind); 16-byte aligned pointers (token_gate 4).  There is no status word: a row whose
- * copy does not arrive within the library's limit on waits is NaN.  One launch. */
+ * copy does not arrive within the library's limit on waits is NaN in every output, and so may be the
+ * rows that its block takes after it.  One launch. */
 int mok_sandwich_norm(const mok_sandwich *args, int64_t T, int d, const void *x,
                       const void *residual, void *residual_out, void *y, void *codes, void *scales,
                       int scale_layout, void *x_codes, void *x_scales, void *h_codes,
@@ -589,6 +590,12 @@ int mok_dispatch_index_noalloc(const mok_dims *dims, const int32_t *topk_idx, co
  * so the context stays usable.  It exercises the error path of the kernels' waits without
  * faulting or hanging the GPU. */
 int mok_selftest_bounded_wait(void *ws, int64_t budget_ns, mok_stream_t stream);
+
+/* Failure-detection self-test of the norms on both sides: the next launch of mok_sandwich_norm by the
+ * calling host thread leaves out the copies of rows `first` and above and gives every wait budget_ns (at most
+ * 2 s), so that the waits for these rows run out, as for copies that do not arrive.  (No effect for d >
+ * 16384, where rows are read without such copies.)  first -1 withdraws it. */
+int mok_selftest_lost_rows(int64_t first, int64_t budget_ns);
 
 /* Kernel timing for benchmarks.  While enabled on the calling host thread, every entry point
  * records a CUDA event pair around each kernel it launches, on the launch stream (the events do

@@ -48,6 +48,7 @@ EXPORTED_SYMBOLS = [
     "mok_select_experts", "mok_select_experts_backward", "mok_moe_backward_select",
     "mok_sandwich_norm", "mok_sandwich_norm_workspace_size", "mok_sandwich_norm_backward",
     "mok_activation_pack", "mok_activation_unpack", "mok_packed_saved_size", "mok_saved_pack", "mok_saved_unpack",
+    "mok_selftest_lost_rows",
 ]
 
 
@@ -143,6 +144,7 @@ def lib():
             "mok_last_launch_count": (ctypes.c_int, []),
             "mok_timing_enable": (ctypes.c_int, [ctypes.c_int]),
             "mok_selftest_bounded_wait": (ctypes.c_int, [_VP, ctypes.c_int64, _VP]),
+            "mok_selftest_lost_rows": (ctypes.c_int, [_I64, _I64]),
             "mok_mx_quantize_rows": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int, _VP, _VP, _VP, _VP]),
             "mok_dispatch_index_noalloc": (ctypes.c_int, [_DP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
             "mok_set_forward_schedule": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_int)]),
@@ -265,6 +267,12 @@ def selftest_bounded_wait(ws, budget_ns=50_000_000):
     """Runs a kernel whose bounded wait must run out; the status word of ws then reads
     MOK_ERR_TIMEOUT (-5)."""
     _check(lib().mok_selftest_bounded_wait(_ptr(ws), int(budget_ns), _stream()))
+
+
+def selftest_lost_rows(first, budget_ns=20_000_000):
+    """The next :func:`sandwich_norm` of this thread runs as if the copies of rows ``first`` and above did
+    not arrive."""
+    _check(lib().mok_selftest_lost_rows(int(first), int(budget_ns)))
 
 
 SCHEDULE_TWO_LAUNCHES, SCHEDULE_FUSED = 0, 1

@@ -39,6 +39,8 @@ struct SandwichParams {
   int d;
   float eps, inv_d, res_scale;
   int post_f32, gate_f32, weight_f32, atoms, depth;
+  int fetched;               // rows that are fetched: T, or fewer in the self-test
+  uint64_t budget;           // of a wait, ns
 };
 
 // Sums of two values over the row's threads, the same in all of them: a row is a block's, of at most 16
@@ -81,7 +83,6 @@ struct RowRing {
   uint32_t base, place, bars;  // first place, bytes of one, first barrier
   int depth, slot;
   uint32_t phase;
-  bool ok;                     // no wait has run out (its row is then made NaN, not left to chance)
   __device__ __forceinline__ uint32_t at(int ahead) const {  // place of the row `ahead` of the present one
     int k = slot + ahead;
     if (k >= depth) k -= depth;
@@ -92,8 +93,8 @@ struct RowRing {
     if (k >= depth) k -= depth;
     return bars + 8 * k;
   }
-  __device__ __forceinline__ void wait(int ahead, volatile int* abort) {
-    ok &= mbar_wait(bar(ahead), slot + ahead >= depth ? phase ^ 1 : phase, nullptr, abort);
+  __device__ __forceinline__ bool wait(int ahead, volatile int* abort, uint64_t budget) const {
+    return mbar_wait(bar(ahead), slot + ahead >= depth ? phase ^ 1 : phase, nullptr, abort, budget);
   }
   __device__ __forceinline__ void next() {
     if (++slot == depth) {
@@ -109,6 +110,54 @@ __device__ __forceinline__ Pairs row_pairs(uint32_t at, int v) {  // vector v of
   r.u[0] = ring16(at + 32 * v);
   r.u[1] = ring16(at + 32 * v + 16);
   return pairs(value8<true>(r));
+}
+
+// For the threads of a row where a wait ran out: `lost` is this thread's first row that it has not seen
+// arrive, or kNoRow.  The rows from the first such row on become NaN in every output.  Copies that may still be
+// under way write to shared memory, so the block does not end before they have landed (or the limit on
+// waits has run out once more).
+constexpr int kNoRow = 0x7fffffff;
+template <bool F32>
+__device__ __noinline__ void lose_rows(const SandwichParams& p, uint32_t bars, int lost) {
+  __shared__ int s_first;
+  const int step = gridDim.x * blockDim.y, begin = blockIdx.x * blockDim.y + threadIdx.y, nvec = p.d >> 3;
+  if (threadIdx.x == 0 && lost != kNoRow) {  // it fetches up to depth - 1 rows past the one that it has last seen
+    const int n = (lost - begin) / step;
+    for (int i = n; i < (n ? n + p.depth - 1 : p.depth) && begin + (int64_t)i * step < p.fetched; ++i) {
+      int none = 0;
+      mbar_wait(bars + 8 * (i % p.depth), (i / p.depth) & 1, nullptr, &none, p.budget);
+    }
+  }
+  lost = __reduce_min_sync(0xffffffffu, lost);
+  if (blockDim.x > 32) {
+    if (threadIdx.x == 0) s_first = kNoRow;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) atomicMin(&s_first, lost);
+    __syncthreads();
+    lost = s_first;
+  }
+  Pairs a;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a.p[j] = both(NAN);
+  auto codes = [&](void* c, uint8_t* scales, int64_t at, int64_t s, int v) {
+    static_cast<uint2*>(c)[at] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    if ((v & 3) == 0) scales[s] = 0;
+  };
+  for (int64_t t = lost; t < p.T; t += step) {
+    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+      const int64_t at = t * nvec + v;
+      store_pairs<F32>(p.residual_out, at, a);
+      if (p.y) store_pairs<false>(p.y, at, a);
+      if (p.codes) {
+        const int b = v >> 2;
+        codes(p.codes, p.scales, at, p.atoms ? sf_atom_word(t >> 7, b >> 2, p.d / 128, t & 127) + (b & 3) : at >> 2, v);
+      }
+      if (p.x_codes) {
+        codes(p.x_codes, p.x_scales, at, at >> 2, v);
+        codes(p.h_codes, p.h_scales, at, at >> 2, v);
+      }
+    }
+  }
 }
 
 // V vectors of eight per thread, MT threads at most.  Sum h^2 follows from sum x^2, which is taken beside
@@ -130,7 +179,8 @@ __global__ void __launch_bounds__(MT, V == 1 || MT <= 320 ? 2 : 1) sandwich_kern
   const int64_t row_step = (int64_t)step * nvec;
   constexpr int kRes = F32 ? 32 : 16;
   constexpr bool kHold = V <= 2;  // the weights in registers; else read where they are used
-  RowRing q{smem_u32(ring) + threadIdx.y * p.depth * (16 + kRes) * nvec, (16u + kRes) * nvec, smem_u32(bars[threadIdx.y]), p.depth, 0, 0, true};
+  RowRing q{smem_u32(ring) + threadIdx.y * p.depth * (16 + kRes) * nvec, (16u + kRes) * nvec, smem_u32(bars[threadIdx.y]), p.depth, 0, 0};
+  int lost = kNoRow;
   bool in[V];
   Pairs W[kHold ? V : 1], w2[kHold ? V : 1];
   auto inner = [&](int v, bool ok) {  // post gate
@@ -144,7 +194,7 @@ __global__ void __launch_bounds__(MT, V == 1 || MT <= 320 ? 2 : 1) sandwich_kern
   };
   // the row `ahead` of the present one; every read of what is in its place has ended
   auto fetch = [&](int ahead) {
-    if (RING && threadIdx.x == 0 && t + (int64_t)ahead * step < T) {
+    if (RING && threadIdx.x == 0 && t + (int64_t)ahead * step < p.fetched && lost == kNoRow) {
       const int64_t from = row + ahead * row_step;
       const uint32_t at = ahead == q.depth ? q.at(0) : q.at(ahead), bar = ahead == q.depth ? q.bar(0) : q.bar(ahead);
       mbar_arrive_expect_tx(bar, q.place);
@@ -166,7 +216,7 @@ __global__ void __launch_bounds__(MT, V == 1 || MT <= 320 ? 2 : 1) sandwich_kern
         for (int j = 0; j < 4; ++j) ss = __ffma2_rn(a.p[j], a.p[j], ss);
       }
     }
-    return q.ok ? ss.x + ss.y : NAN;
+    return ss.x + ss.y;
   };
 #pragma unroll
   for (int i = 0; i < V; ++i) in[i] = i < V - 1 || threadIdx.x + i * blockDim.x < nvec;  // only the last can be past the row
@@ -188,7 +238,7 @@ __global__ void __launch_bounds__(MT, V == 1 || MT <= 320 ? 2 : 1) sandwich_kern
   }
   float sums[2] = {0.0f, 0.0f};
   if (t < T) {
-    if constexpr (RING) q.wait(0, &s_abort);
+    if constexpr (RING) lost = q.wait(0, &s_abort, p.budget) ? kNoRow : t;
     sums[1] = square_of(row, 0);
   }
   row_sums(sums, smem, 1);
@@ -225,7 +275,7 @@ __global__ void __launch_bounds__(MT, V == 1 || MT <= 320 ? 2 : 1) sandwich_kern
     sums[0] = ss.x + ss.y;
     sums[1] = 0.0f;
     if (more) {
-      if constexpr (RING) q.wait(1, &s_abort);
+      if constexpr (RING) lost = q.wait(1, &s_abort, p.budget) ? lost : min(lost, t + step);
       sums[1] = square_of(row + row_step, 1);
     }
     row_sums(sums, smem, turn);
@@ -252,6 +302,8 @@ __global__ void __launch_bounds__(MT, V == 1 || MT <= 320 ? 2 : 1) sandwich_kern
     row += row_step;
     q.next();
   }
+  if (RING && (blockDim.x > 32 ? __syncthreads_or(lost != kNoRow) : __any_sync(0xffffffffu, lost != kNoRow)))
+    lose_rows<F32>(p, q.bars, lost);
   for (int64_t r = t; r < p.rows; r += step)  // padding rows of the scale atoms
     for (int kb = threadIdx.x; kb < p.d / 128; kb += blockDim.x)
       *reinterpret_cast<uint32_t*>(p.scales + sf_atom_word(r >> 7, kb, p.d / 128, (int)(r & 127))) = 0;
@@ -635,6 +687,14 @@ __global__ void __launch_bounds__(32 * kSumWarps) sandwich_sum_kernel(const __gr
   }
 }
 
+// What mok_selftest_lost_rows asks of the next call of this host thread.
+struct LostRows {
+  int64_t first = -1;
+  uint64_t budget = kWaitNs;
+  int fetched(int64_t T) const { return (int)(first < 0 ? T : std::min(first, T)); }
+};
+static thread_local LostRows g_lost_rows;
+
 static bool sandwich_sizes_ok(int64_t T, int d) {
   return T >= 0 && T <= 0x7fffffffLL / 8 && d > 0 && d <= kSandwichMaxD && d % 8 == 0;
 }
@@ -651,7 +711,7 @@ constexpr int kSmemOwn = 3 * 1024;      // of a block: reserved and static
 constexpr int kPlainSmem = 40 * 1024;   // dynamic bytes that need no attribute
 constexpr int kWideThreads = 512;       // of a block with two vectors per thread and more: 128 registers each
 // Forward: one vector per thread up to 512 threads, of which 1024 fit an SM (64 registers): 2^25 elements
-// with a bf16 residual at d = 4096 in 45 us, 61 with one block per SM, 40 at the copy rate.  With two
+// with a bf16 residual at d = 4096 in 46 us, 61 with one block per SM, 40 at the copy rate.  With two
 // vectors two blocks fit up to 320 threads (96 registers): T = 8192, d = 5120 58 us, 61 with one.
 static SandwichShape sandwich_shape(int d) {
   SandwichShape n;
@@ -700,6 +760,13 @@ static cudaError_t allow_smem(K k, int64_t smem) {
 
 extern "C" {
 
+int mok_selftest_lost_rows(int64_t first, int64_t budget_ns) {
+  if (first < -1 || budget_ns <= 0 || budget_ns > (int64_t)mok::kWaitNs) return MOK_ERR_INVALID_ARG;
+  mok::g_lost_rows.first = first;
+  mok::g_lost_rows.budget = first < 0 ? mok::kWaitNs : (uint64_t)budget_ns;
+  return MOK_OK;
+}
+
 int mok_sandwich_norm(const mok_sandwich* a, int64_t T, int d, const void* x, const void* residual, void* residual_out,
                       void* y, void* codes, void* scales, int scale_layout, void* x_codes, void* x_scales,
                       void* h_codes, void* h_scales, mok_stream_t stream) {
@@ -727,7 +794,8 @@ int mok_sandwich_norm(const mok_sandwich* a, int64_t T, int d, const void* x, co
                    static_cast<uint8_t*>(scales), x_codes, static_cast<uint8_t*>(x_scales), h_codes,
                    static_cast<uint8_t*>(h_scales), T, T, d, a->eps, 1.0f / (float)d, a->res_scale,
                    a->post_type == MOK_T_F32, a->gate_type == MOK_T_F32, a->weight_type == MOK_T_F32,
-                   scale_layout == MOK_SCALES_ATOMS, 0};
+                   scale_layout == MOK_SCALES_ATOMS, 0, g_lost_rows.fetched(T), g_lost_rows.budget};
+  g_lost_rows = LostRows();
   if (codes && p.atoms) p.rows = (T + 127) / 128 * 128;
   const int sms = num_sms();
   const SandwichShape n = sandwich_shape(d);
