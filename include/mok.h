@@ -500,8 +500,10 @@ size_t mok_sandwich_norm_workspace_size(int64_t T, int d);
  *   wrote them: the gradients are then those at the values that these hold.
  *   -> dx[T,d] bf16, dresidual[T,d] of res_type, dpost_weight[d], dgate[d] (with gate),
  *      dtoken_gate[T] (with token_gate), dweight[d] (with weight) fp32.
- * dx may be dy, dresidual may be dres.  Sizes, alignment and waits as in mok_sandwich_norm.  Two
- * launches, the second begins under the first. */
+ * dx may be dy, dresidual may be dres.  Sizes and alignment as in mok_sandwich_norm.  Where a wait runs
+ * out, the status word of ws (zeroed once) becomes MOK_ERR_TIMEOUT, the row in question and those that
+ * its block takes after it are NaN in dx, dresidual and dtoken_gate, and so are the gradients of the
+ * weights.  Two launches, the second begins under the first. */
 int mok_sandwich_norm_backward(const mok_sandwich *args, int64_t T, int d, const void *dy,
                                const void *dres, const void *x, const void *x_scales, const void *h,
                                const void *h_scales, void *dx, void *dresidual, float *dpost_weight,
@@ -591,10 +593,11 @@ int mok_dispatch_index_noalloc(const mok_dims *dims, const int32_t *topk_idx, co
  * faulting or hanging the GPU. */
 int mok_selftest_bounded_wait(void *ws, int64_t budget_ns, mok_stream_t stream);
 
-/* Failure-detection self-test of the norms on both sides: the next launch of mok_sandwich_norm by the
- * calling host thread leaves out the copies of rows `first` and above and gives every wait budget_ns (at most
- * 2 s), so that the waits for these rows run out, as for copies that do not arrive.  (No effect for d >
- * 16384, where rows are read without such copies.)  first -1 withdraws it. */
+/* Failure-detection self-test of the norms on both sides: the next launch of mok_sandwich_norm or of
+ * mok_sandwich_norm_backward by the calling host thread leaves out the copies of rows `first` and above
+ * and gives every wait for a row budget_ns (at most 2 s), so that the waits for these rows run out, as
+ * for copies that do not arrive.  (No effect on rows so wide that they are read without such copies.)
+ * first -1 withdraws it. */
 int mok_selftest_lost_rows(int64_t first, int64_t budget_ns);
 
 /* Kernel timing for benchmarks.  While enabled on the calling host thread, every entry point

@@ -270,8 +270,8 @@ def selftest_bounded_wait(ws, budget_ns=50_000_000):
 
 
 def selftest_lost_rows(first, budget_ns=20_000_000):
-    """The next :func:`sandwich_norm` of this thread runs as if the copies of rows ``first`` and above did
-    not arrive."""
+    """The next :func:`sandwich_norm` or :func:`sandwich_norm_backward` of this thread runs as if the
+    copies of rows ``first`` and above did not arrive."""
     _check(lib().mok_selftest_lost_rows(int(first), int(budget_ns)))
 
 
@@ -563,8 +563,8 @@ def sandwich_norm_backward(x, h, post_weight, dy=None, dres=None, weight=None, g
     tuple (codes, scales) of its 8-bit form; h None without weight.  ``residual_dtype``: the residual's
     type where neither h nor dres tells it (default bf16).  Returns a dict: "dx" [T,d] bf16,
     "dresidual" [T,d] in the residual's type, fp32 "dpost_weight" [d] and, for those given, "dweight"
-    [d], "dgate" [d], "dtoken_gate" [T].  ``ws``: at least sandwich_norm_workspace_size(T, d) bytes
-    (allocated per call when None)."""
+    [d], "dgate" [d], "dtoken_gate" [T].  ``ws``: at least sandwich_norm_workspace_size(T, d) bytes,
+    zeroed once, whose status word reports waits that ran out (allocated per call when None)."""
     packed = isinstance(x, tuple)
     rows, x_scales = x if packed else (x, None)
     if rows.dim() != 2:

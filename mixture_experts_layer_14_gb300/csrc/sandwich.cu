@@ -118,7 +118,7 @@ __device__ __forceinline__ Pairs row_pairs(uint32_t at, int v) {  // vector v of
 // waits has run out once more).
 constexpr int kNoRow = 0x7fffffff;
 template <bool F32>
-__device__ __noinline__ void lose_rows(const SandwichParams& p, uint32_t bars, int lost) {
+__device__ __forceinline__ void lose_rows(const SandwichParams& p, uint32_t bars, int lost) {
   __shared__ int s_first;
   const int step = gridDim.x * blockDim.y, begin = blockIdx.x * blockDim.y + threadIdx.y, nvec = p.d >> 3;
   if (threadIdx.x == 0 && lost != kNoRow) {  // it fetches up to depth - 1 rows past the one that it has last seen
@@ -324,11 +324,36 @@ struct SandwichBwdParams {
   void* dresidual;
   float* dtoken_gate;      // or NULL
   float* partial;          // [2][grid][d]: A, dweight
+  int* status;
   int64_t T;
   int d;
   float eps, inv_d, res_scale;
   int post_f32, gate_f32, weight_f32, depth;
+  int fetched;             // rows that are fetched: T, or fewer in the self-test
+  uint64_t budget;         // of a wait for a row, ns
 };
+
+// NaN in every output of the rows t, t + gridDim.x, ... and in the block's sums over rows, each thread its
+// columns of the backward pass.
+template <bool F32>
+__device__ __forceinline__ void lose_bwd_rows(const SandwichBwdParams& p, int64_t t, int threads) {
+  const int nvec = p.d >> 3;
+  Pairs a;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a.p[j] = both(NAN);
+  for (; t < p.T; t += gridDim.x) {
+    for (int v = threadIdx.x; v < nvec; v += threads) {
+      store_pairs<F32>(p.dresidual, t * nvec + v, a);
+      store_pairs<false>(p.dx, t * nvec + v, a);
+    }
+    if (p.dtoken_gate && threadIdx.x == 0) p.dtoken_gate[t] = NAN;
+  }
+  float* mine = p.partial + (int64_t)blockIdx.x * p.d;
+  for (int v = threadIdx.x; v < nvec; v += threads) {
+    store_pairs<true>(mine, v, a);
+    if (p.dy) store_pairs<true>(mine + (int64_t)gridDim.x * p.d, v, a);
+  }
+}
 
 // Six sums of a row (an array of eight, two of them empty) over the consumer warps.  In put_sums every step
 // of the tree halves the number of values that a lane still has; the four lanes of value i then hold its
@@ -375,7 +400,8 @@ template <int V, bool F32, bool PACKED, bool RING, int MT>
 __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p) {
   __shared__ __align__(16) float smem[2][8][16];
   __shared__ __align__(8) uint64_t s_bars[7];  // full and empty, three each; the exchange
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_stuck;  // a wait for a row, for the exchange has run out
+  __shared__ int s_lost;            // the first row that a thread has not seen arrive
   extern __shared__ __align__(16) uint8_t ring[];
   const int nvec = p.d >> 3, T = (int)p.T;
   const int threads = RING ? blockDim.x - 32 : blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -398,7 +424,8 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
       mbar_init(empty + 8 * k, threads >> 5);
     }
     mbar_init(exchange, threads >> 5);
-    s_abort = 0;
+    s_abort = s_stuck = 0;
+    s_lost = kNoRow;
     fence_barrier_init();
   }
   for (int i = threadIdx.x; i < 256; i += blockDim.x) (&smem[0][0][0])[i] = 0.0f;
@@ -407,13 +434,14 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
   if (RING && (int)threadIdx.x >= threads) {
     // The producer.  A row's scales need not be whole 16 bytes: those around them are copied, up to the
     // last whole ones of the tensor; what is left at its end is stored before the arrival that others
-    // wait for.
+    // wait for.  It stays until its last copies have landed (or the limit on waits has run out), also where
+    // the others wait no longer.
     const int64_t scale_end = PACKED ? ((p.T * nvec) >> 2) & ~(int64_t)15 : 0;
     if (lane == 0) {
-      int k = 0;
+      int k = 0, n = 0;
       uint32_t phase = 1;  // a place's first wait ends at once
-      for (; t < T; t += gridDim.x, row += row_step) {
-        if (!mbar_wait(empty + 8 * k, phase, nullptr, &s_abort)) break;
+      for (; t < p.fetched; t += gridDim.x, row += row_step, ++n) {
+        if (!mbar_wait(empty + 8 * k, phase, p.status, &s_abort, p.budget)) break;
         const uint32_t at = base + k * place, bar = full + 8 * k;
         const int64_t s0 = (row >> 2) & ~(int64_t)15, s1 = min((((row + nvec) >> 2) + 15) & ~(int64_t)15, scale_end);
         const uint32_t scales = PACKED && s1 > s0 ? (uint32_t)(s1 - s0) : 0;
@@ -435,6 +463,10 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
           k = 0;
           phase ^= 1;
         }
+      }
+      for (int i = max(0, n - p.depth); i < n; ++i) {
+        int none = 0;
+        mbar_wait(full + 8 * (i % p.depth), (i / p.depth) & 1, p.status, &none, p.budget);
       }
     }
     return;
@@ -491,7 +523,6 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
     else if constexpr (RING) return row_pairs<false>(at + x_at, v);
     else return pairs(load8<false>(p.x, from + v));
   };
-  bool ok = true;  // no wait has run out (rows are then made NaN, not left to chance)
   // first pass: h h, g h, x x, g W x, h W x, dres W x
   auto first = [&](int64_t from, uint32_t at, int turn) {
     float2 s[6];
@@ -530,7 +561,6 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < 6; ++k) a[k] = s[k].x + s[k].y;
     a[6] = a[7] = 0.0f;
-    if (!ok) a[2] = NAN;
     put_sums(a, smem[turn], warp);
     __syncwarp();
     if (lane == 0) mbar_arrive(exchange);
@@ -552,9 +582,12 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
   const float2 a2 = both(p.res_scale);
   uint32_t at = base, phase = 0;  // the row's place in the ring and its phase
   int k = 0, turn = 0;
-  if constexpr (RING) ok &= mbar_wait(full, 0, nullptr, &s_abort);
+  // Every warp arrives on the exchange once its wait for the row has ended, so that the wait for the
+  // others runs out later than theirs and does not heed s_abort.
+  if constexpr (RING)
+    if (!mbar_wait(full, 0, p.status, &s_abort, p.budget)) atomicMin(&s_lost, t);
   first(row, at, 0);
-  ok &= mbar_wait(exchange, 0, nullptr, &s_abort);
+  if (!mbar_wait(exchange, 0, p.status, &s_stuck, 2 * p.budget)) atomicMin(&s_lost, t);
   get_sums(sums, smem[0]);
   while (true) {
     const bool more = t + (int)gridDim.x < T;
@@ -564,7 +597,8 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
     auto ahead = [&]() {
       if (!more) return;
       if (p.token_gate) next_gate = p.token_gate[t + gridDim.x];
-      if constexpr (RING) ok &= mbar_wait(full + 8 * next_k, next_phase, nullptr, &s_abort);
+      if constexpr (RING)
+        if (!mbar_wait(full + 8 * next_k, next_phase, p.status, &s_abort, p.budget)) atomicMin(&s_lost, t + (int)gridDim.x);
       first(row + row_step, next_at, turn);
     };
     if constexpr (!kLate) ahead();
@@ -604,10 +638,10 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
     }
     if constexpr (kLate) ahead();
     if (!more) break;
-    ok &= mbar_wait(exchange, turn, nullptr, &s_abort);
+    t += gridDim.x;
+    if (!mbar_wait(exchange, turn, p.status, &s_stuck, 2 * p.budget)) atomicMin(&s_lost, t);
     get_sums(sums, smem[turn]);
     gate = next_gate;
-    t += gridDim.x;
     row += row_step;
     k = next_k;
     phase = next_phase;
@@ -623,6 +657,8 @@ __global__ void __launch_bounds__(MT) sandwich_bwd_kernel(const __grid_constant_
       if (next_norm) store_pairs<true>(mine + (int64_t)gridDim.x * p.d, v, dw[i]);
     }
   }
+  asm volatile("barrier.cta.sync 1, %0;" ::"r"(threads) : "memory");  // the producer has no part in it
+  if (s_lost != kNoRow) lose_bwd_rows<F32>(p, s_lost, threads);
 }
 
 // Sums the n partial rows of A (blockIdx.y == 0) and of dweight (1) in a fixed order.  A block takes 32
@@ -711,7 +747,7 @@ constexpr int kSmemOwn = 3 * 1024;      // of a block: reserved and static
 constexpr int kPlainSmem = 40 * 1024;   // dynamic bytes that need no attribute
 constexpr int kWideThreads = 512;       // of a block with two vectors per thread and more: 128 registers each
 // Forward: one vector per thread up to 512 threads, of which 1024 fit an SM (64 registers): 2^25 elements
-// with a bf16 residual at d = 4096 in 46 us, 61 with one block per SM, 40 at the copy rate.  With two
+// with a bf16 residual at d = 4096 in 45 us, 61 with one block per SM, 40 at the copy rate.  With two
 // vectors two blocks fit up to 320 threads (96 registers): T = 8192, d = 5120 58 us, 61 with one.
 static SandwichShape sandwich_shape(int d) {
   SandwichShape n;
@@ -865,9 +901,10 @@ int mok_sandwich_norm_backward(const mok_sandwich* a, int64_t T, int d, const vo
   const bool f32 = a->res_type == MOK_T_F32;
   float* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
   SandwichBwdParams p{dy, h, static_cast<const uint8_t*>(h_scales), x, static_cast<const uint8_t*>(x_scales), dres,
-                      a->post_weight, a->gate, a->token_gate, a->weight, dx, dresidual, dtoken_gate, partial, T, d, a->eps,
-                      1.0f / (float)d, a->res_scale, a->post_type == MOK_T_F32, a->gate_type == MOK_T_F32,
-                      a->weight_type == MOK_T_F32, 0};
+                      a->post_weight, a->gate, a->token_gate, a->weight, dx, dresidual, dtoken_gate, partial,
+                      static_cast<int*>(ws), T, d, a->eps, 1.0f / (float)d, a->res_scale, a->post_type == MOK_T_F32,
+                      a->gate_type == MOK_T_F32, a->weight_type == MOK_T_F32, 0, g_lost_rows.fetched(T), g_lost_rows.budget};
+  g_lost_rows = LostRows();
   const SandwichShape n = sandwich_bwd_shape(d);
   const int64_t nvec = d / 8, res = f32 ? 32 : 16;
   const int64_t scales = packed ? (nvec / 4 + 31) / 16 * 16 : 0;  // as the kernel lays a place out

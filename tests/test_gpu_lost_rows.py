@@ -61,3 +61,32 @@ def test_withdrawn_and_refused():
     mok.selftest_lost_rows(3)
     mok.selftest_lost_rows(-1)
     assert not mok.sandwich_norm(v["x"], v["r"], v["post"])["residual"].isnan().any()
+
+
+@pytest.mark.parametrize("T,d,res,first", CASES[:-1] + [(330, 8192, "bf16", 160), (400, 9216, "bf16", 155)])
+@pytest.mark.parametrize("next_norm,dh,packed", [(True, True, False), (False, True, False), (True, False, True), (False, True, True)])
+def test_backward(T, d, res, first, next_norm, dh, packed):
+    """Lost rows are NaN in dx, dresidual and the token gate's gradient, and so are the weights' gradients;
+    the status word says why."""
+    ensure_lib()
+    v = _make(T, d, res)
+    dy, tg = _make(T, d, res, 4)["x"], torch.rand(T, device="cuda")
+    x, h = (mok.activation_pack(v["x"]), mok.activation_pack(v["r"])) if packed else (v["x"], v["r"])
+    ws = torch.zeros(mok.sandwich_norm_workspace_size(T, d), dtype=torch.uint8, device="cuda")
+
+    def run():
+        return mok.sandwich_norm_backward(
+            x, h if next_norm else None, v["post"], dy=dy if next_norm else None, dres=v["r"] if dh else None,
+            weight=v["w"] if next_norm else None, token_gate=tg, residual_dtype=v["r"].dtype, ws=ws)
+    clean = run()
+    assert mok.read_status(ws) == 0 and not any(t.isnan().any() for t in clean.values())
+    mok.selftest_lost_rows(first)
+    out = run()
+    assert mok.read_status(ws) == -5  # MOK_ERR_TIMEOUT
+    for k in ("dx", "dresidual", "dtoken_gate"):
+        assert out[k][first:].isnan().all() and torch.equal(out[k][:first], clean[k][:first]), k
+    for k in set(out) - {"dx", "dresidual", "dtoken_gate"}:
+        assert out[k].isnan().all(), k
+    mok.clear_status(ws)
+    again = run()
+    assert mok.read_status(ws) == 0 and all(torch.equal(again[k], clean[k]) for k in clean)
