@@ -7,10 +7,11 @@
 // A warp takes a token, a lane a run of neighbouring experts of one group, in ascending order.  The
 // k-th largest of the lanes' own largest keys is a lower limit of the k-th key, which leaves about
 // k + 2 candidates (their expected number, 32 (H(32) - H(32 - k)), is 9.1 for k = 8); these go
-// to a lane each and are ranked by counting.  Which of two experts is chosen is decided as in exact
-// arithmetic: where two keys that the choice depends on are nearer than fp32 can tell (a few tokens
-// in a thousand) the experts in question are ranked again in 64 bits.  Without a bias scores rise
-// with the logits, which are ranked themselves.
+// to a lane each and are ranked by counting.  Which of two experts is chosen does not depend on fp32
+// roundings: where two keys that the choice depends on are nearer than fp32 can tell (a few tokens
+// in a thousand) the experts in question are ranked again in 64 bits, and keys that are equal there by their
+// logits, with which scores rise (a sigmoid is 1 in 64 bits from 37 on).  Without a bias the logits are
+// ranked themselves.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -121,9 +122,10 @@ __device__ __noinline__ double exact_sum(SelectRow<SOFTMAX, BIAS> r, int E) {
   return z;
 }
 
-// The k best experts of [lo, hi) in exact order among those with keys[e] >= threshold (k <= 8);
-// lane j < k returns the j-th (index -1: there is none).  `list` holds hi - lo numbers.  Up to 32 are
-// ranked by counting; more of them (many equal numbers) come 24 to a round beside the best so far.
+// The k best experts of [lo, hi) in exact order (64-bit key, logit, lower index) among those with keys[e] >=
+// threshold (k <= 8); lane j < k returns the j-th (index -1: there is none).  `list` holds hi - lo numbers.
+// Up to 32 are ranked by counting; more of them (many equal numbers) come 24 to a round beside the best
+// so far.
 template <bool SOFTMAX, bool BIAS>
 __device__ __noinline__ int exact_best(SelectRow<SOFTMAX, BIAS> r, double sum, const float* keys, int* list, int lo, int hi,
                                        float threshold, int k, double* key_out) {
@@ -139,6 +141,11 @@ __device__ __noinline__ int exact_best(SelectRow<SOFTMAX, BIAS> r, double sum, c
   __syncwarp();
   int idx = -1;
   double key = 0.0;
+  // Of experts a and b with equal keys, whether a comes first.
+  auto first = [&](int a, int b) {
+    const float la = r.logits[a], lb = r.logits[b];
+    return keys[a] != kMasked && la != lb ? la > lb : a < b;
+  };
   if (count <= 32) {  // a lane each, in ascending order
     if (lane < count) {
       idx = list[lane];
@@ -147,7 +154,7 @@ __device__ __noinline__ int exact_best(SelectRow<SOFTMAX, BIAS> r, double sum, c
     int place = 0;
     for (int j = 0; j < count; ++j) {
       const double o = __shfl_sync(kAll, key, j);
-      place += o > key || (o == key && j < lane);
+      place += o > key || (o == key && j != lane && lane < count && first(list[j], idx));
     }
     __syncwarp();
     if (lane < count) list[place] = lane;
@@ -172,7 +179,7 @@ __device__ __noinline__ int exact_best(SelectRow<SOFTMAX, BIAS> r, double sum, c
       for (int o = 16; o; o >>= 1) {
         const double ok = __shfl_xor_sync(kAll, bk, o);
         const int oi = __shfl_xor_sync(kAll, bi, o);
-        const bool take = oi >= 0 && (bi < 0 || ok > bk || (ok == bk && oi < bi));
+        const bool take = oi >= 0 && (bi < 0 || ok > bk || (ok == bk && first(oi, bi)));
         if (take) { bk = ok; bi = oi; }
       }
       if (bi >= 0 && idx == bi) idx = -1;
@@ -187,7 +194,8 @@ __device__ __noinline__ int exact_best(SelectRow<SOFTMAX, BIAS> r, double sum, c
 }
 
 // Whether this lane's group stays, where fp32 scores of one that stays and one that goes are within
-// slack: groups farther than that from both keep their fp32 score, the others get exact ones.
+// slack: groups farther than that from both keep their fp32 score, the others get exact ones.  Largest keys
+// that are equal in 64 bits go by their logits, sums of two to the lower group.
 template <bool SOFTMAX, bool BIAS>
 __device__ __noinline__ bool exact_groups(SelectRow<SOFTMAX, BIAS> r, const SelectParams& p, float* keys, int* list, float err,
                                           float score, float second, float in, float out, float slack) {
@@ -196,6 +204,7 @@ __device__ __noinline__ bool exact_groups(SelectRow<SOFTMAX, BIAS> r, const Sele
   const double sum = exact_sum(r, p.E);
   __syncwarp();
   double mine = score > -INFINITY ? (double)score : -1e300;
+  float mine_l = 0.0f;
   for (int g = 0; g < p.groups; ++g) {
     const float sc = __shfl_sync(kAll, score, g << p.log_lanes), low = __shfl_sync(kAll, second, g << p.log_lanes);
     if (!(sc > -INFINITY) || sc - in > slack || out - sc > slack) continue;
@@ -203,13 +212,17 @@ __device__ __noinline__ bool exact_groups(SelectRow<SOFTMAX, BIAS> r, const Sele
     const int e = exact_best(r, sum, keys, list, g * p.n, (g + 1) * p.n, low - 2.0f * err - 0x1p-22f * fabsf(low),
                              p.top2 ? 2 : 1, &key);
     const double k1 = __shfl_sync(kAll, key, 0), k2 = __shfl_sync(kAll, key, 1);
-    const int e2 = __shfl_sync(kAll, e, 1);
-    if (group == g) mine = p.top2 && e2 >= 0 ? k1 + k2 : k1;
+    const int e1 = __shfl_sync(kAll, e, 0), e2 = __shfl_sync(kAll, e, 1);
+    if (group == g) {
+      mine = p.top2 && e2 >= 0 ? k1 + k2 : k1;
+      mine_l = p.top2 || e1 < 0 ? 0.0f : r.logits[e1];
+    }
   }
   int rank = 0;
   for (int g = 0; g < p.groups; ++g) {
     const double other = __shfl_sync(kAll, mine, g << p.log_lanes);
-    rank += other > mine || (other == mine && g < group);
+    const float other_l = __shfl_sync(kAll, mine_l, g << p.log_lanes);
+    rank += other > mine || (other == mine && (other_l > mine_l || (other_l == mine_l && g < group)));
   }
   return rank < p.kept;
 }
