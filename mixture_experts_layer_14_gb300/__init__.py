@@ -662,8 +662,9 @@ def balance_loss(D, logits, topk_idx, ws, alpha, z_coef=0.0, seq_offsets=None, t
 def select_experts(D, sel, logits, ws, bias=None):
     """Experts and weights of every token from logits [T,E] fp32 (of :func:`route`) by the rule
     ``sel`` (a :class:`Selection`): (topk_idx [T,k] int32, topk_w [T,k] fp32), for
-    :func:`dispatch_index`.  ``bias`` fp32 [E] is added to the scores for the ranking alone; experts
-    at or below -1e30 in logits or bias are shut off.  ``ws``: any zeroed workspace of at least 256
+    :func:`dispatch_index`.  ``bias`` fp32 [E] is added to the scores for the ranking alone.  Experts
+    whose logit is at or below -1e30 are shut off: chosen last, with weight 0.  A bias at or below -1e30
+    makes its expert the last choice too, but if it is chosen it has its score's weight.  ``ws``: any zeroed workspace of at least 256
     bytes, whose status word reports NaN."""
     dev = logits.device
     _want(logits, "logits", (D.T, D.E), torch.float32, dev)

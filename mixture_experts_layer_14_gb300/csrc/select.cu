@@ -42,8 +42,9 @@ struct SelectParams {
 
 // Keys: kAbsent for a slot without an expert, or whose group is out; kMasked for one that is shut off.
 constexpr float kAbsent = -INFINITY, kMasked = -FLT_MAX;
-// Logits and biases from here on down (-inf, the lowest value of a type) shut an expert off; sums of
-// two biases within +-1e30 stay finite.
+// Logits from here on down (-inf, the lowest value of a type) shut an expert off: it ranks last and weighs
+// 0.  Biases from here on down only rank: the expert is the last choice, with its score.  Sums of two biases
+// within +-1e30 stay finite.
 constexpr float kShutOff = -1e30f;
 
 __device__ __forceinline__ float warp_top(float v) {  // not NaN
