@@ -302,7 +302,8 @@ size_t mok_balance_loss_workspace_size(const mok_dims *dims, int64_t n_seqs);
  *   -> counts[n_seqs,E] int32, loss[2] fp32 = {balance, z}, dlogits[T,E] fp32 (NULL to skip; rows
  *      of left-out tokens are zero, whatever their logits hold).
  * Experts masked with -inf logits get probability and gradient 0; a token all of whose logits are
- * -inf gives no loss and no gradient.  An index outside [0,E) sets MOK_ERR_DEVICE_CHECK in the
+ * -inf gives no loss and no gradient (finite logits are logits, however low: a row of the type's lowest
+ * value is a uniform one with a huge z loss, unless token_mask leaves it out).  An index outside [0,E) sets MOK_ERR_DEVICE_CHECK in the
  * status word of ws and its route is not counted.  dims->T, E, k are used; n_seqs >= 1,
  * n_seqs * E < 2^31; logits, counts, dlogits and ws are 16-byte aligned.  The gradient goes into mok_moe_backward_aux. */
 int mok_balance_loss(const mok_dims *dims, const float *logits, const int32_t *topk_idx,
@@ -438,8 +439,10 @@ int mok_select_experts(const mok_dims *dims, const mok_selection *sel, const flo
  *   scores; sigmoid: scale s_j (1 - s_j) dw_j; softmax: scale s_e (dw_e - sum_i s_i dw_i) for every
  *   expert (dw_e = 0 where e was not chosen); 0 elsewhere.
  * An index outside [0,E) sets MOK_ERR_DEVICE_CHECK in the status word of ws and is left out; routes
- * that name one expert twice add up.  Experts that are shut off get 0.  sel's groups are not used
- * but checked.  logits, dlogits_aux, dlogits and ws are 16-byte aligned; dlogits may be
+ * that name one expert twice add up.  Experts that are shut off get dlogits_aux alone (0 without it):
+ * mok_balance_loss leaves out -inf, but a token all of whose logits are finite is one of its tokens
+ * whatever they are, and at a type's lowest value its z loss is huge or infinite; such tokens are left
+ * out by its token_mask.  sel's groups are not used but checked.  logits, dlogits_aux, dlogits and ws are 16-byte aligned; dlogits may be
  * dlogits_aux.  One launch. */
 int mok_select_experts_backward(const mok_dims *dims, const mok_selection *sel, const float *logits,
                                 const int32_t *topk_idx, const float *dtopk_w,

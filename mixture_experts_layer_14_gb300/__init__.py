@@ -681,7 +681,8 @@ def select_experts(D, sel, logits, ws, bias=None):
 def select_experts_backward(D, sel, logits, topk_idx, dtopk_w, ws, dlogits_aux=None):
     """Gradient of the logits [T,E] fp32 for dtopk_w [T,k] fp32, the gradient of the weights of
     :func:`select_experts` (the choice held constant), plus ``dlogits_aux`` [T,E] (of
-    :func:`balance_loss`).  ``ws`` as in :func:`select_experts`; reports an index outside [0,E)."""
+    :func:`balance_loss`; for experts that are shut off it is the whole gradient).  ``ws`` as in
+    :func:`select_experts`; reports an index outside [0,E)."""
     dev = logits.device
     _want(logits, "logits", (D.T, D.E), torch.float32, dev)
     _want(topk_idx, "topk_idx", (D.T, D.k), torch.int32, dev)
