@@ -164,7 +164,7 @@ __device__ __forceinline__ void lose_rows(const SandwichParams& p, uint32_t bars
 // the row before's sum h^2: one exchange and one barrier per row.  (Writing sum h^2 out in sums of the
 // inputs, as the backward pass does with its sums, would lose rho2 where the branch cancels the residual.)
 // At T = 16384, d = 7168 with a bf16 residual, codes and checkpoint (1.30 GB) 199 us, 98% of the copy
-// rate, 587 instructions per warp and row; with rows by asynchronous copies of the threads' own vectors
+// rate, 562 instructions per warp and row; with rows by asynchronous copies of the threads' own vectors
 // 234 us and 668, with scalar arithmetic and sums in every lane besides 257 and 845.
 template <int V, bool F32, bool RING, int MT>
 __global__ void __launch_bounds__(MT, V == 1 || MT <= 320 ? 2 : 1) sandwich_kernel(const __grid_constant__ SandwichParams p) {
@@ -392,8 +392,8 @@ __device__ __forceinline__ void get_sums(float (&a)[6], float (&smem)[8][16]) {
 // One more warp fetches rows as their places come free.
 // Rows of fp32 without codes, of which only two may fit, take the second pass first, so that the next
 // fetch has the first pass and the exchange to land.
-// At T = 8192, d = 7168 with a gradient through the residual 115 us from bf16 rows (704 MB, 92% of the
-// copy rate) and 124 from codes (591 MB, 71%: 790 instructions per warp and row against 666, at 62% of
+// At T = 8192, d = 7168 with a gradient through the residual 117 us from bf16 rows (704 MB, 90% of the
+// copy rate) and 122.5 from codes (591 MB, 72%: 780 instructions per warp and row, some 120 more, at 62% of
 // the issue slots).  With q summed from ds, in a second exchange per row, 142 us from codes and more than
 // that with the weights in registers, which x, h and ds then share with it (185).
 template <int V, bool F32, bool PACKED, bool RING, int MT>
@@ -761,8 +761,8 @@ static SandwichShape sandwich_shape(int d) {
 // Backward: one warp more fetches (not for the widest rows, which have no ring).  A vector of a thread
 // takes 32 registers across rows (two weights, two sums), so threads get 96 registers with one vector, 128
 // with two, 168 with three, and with that warp a block has no more threads than those allow.  T = 8192 at
-// d = 8192 130 us with three, 287 with four; at d = 7168 from codes 124 with two, 130 with three, 154 with
-// one in 28 warps; 2^25 elements at d = 2048 75 us with two blocks per SM, 121 with one.
+// d = 8192 130 us with three, 287 with four; at d = 7168 from codes 123 with two, 130 with three, 154 with
+// one in 28 warps; 2^25 elements at d = 2048 76 us with two blocks per SM, 121 with one.
 constexpr int kNarrowThreads = 512 + 32, kThreeThreads = 384;
 static SandwichShape sandwich_bwd_shape(int d) {
   SandwichShape n;

@@ -228,8 +228,8 @@ __device__ __noinline__ bool exact_groups(SelectRow<SOFTMAX, BIAS> r, const Sele
   return rank < p.kept;
 }
 
-// Bound by issue and its latencies: at T = 16384, E = 384, k = 8 with sigmoid scores and a bias 18.5 us
-// (12.2 without a bias; 4 at the copy rate), E = 256 with 4 of 8 groups 18.6.  Most of a token's
+// Bound by latencies (64% of the issue slots): at T = 16384, E = 384, k = 8 with sigmoid scores and a bias
+// 18.9 us (12.3 without a bias; 4 at the copy rate), E = 256 with 4 of 8 groups 20-24.  Most of a token's
 // instructions do not depend on E, and 2 tokens in a warp share them but wait longer: 27 us where one
 // took 23.6.  Ranking by rounds of a maximum over the warp 47 us.
 // V: experts of a lane at most.  VEC: groups and runs are whole vectors of four.
