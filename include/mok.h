@@ -418,8 +418,8 @@ typedef struct {
  * Where fp32 cannot tell two keys apart they are computed in 64 bits; of keys that are equal there the
  * one of the larger logit comes first, of equal logits that of the lower index.  Experts of one bias
  * (or none) are so ranked as in exact arithmetic, whatever the logits; where biases differ, 64 bits
- * decide.  Groups likewise by their largest keys; of sums of two that are equal in 64 bits the lower
- * group's comes first.  Experts whose logit is at or below -1e30
+ * decide.  Groups likewise by their largest keys; sums of two are compared in 64 bits, and where these
+ * are equal the lower group comes first.  Experts whose logit is at or below -1e30
  * (-inf, a type's lowest value) are shut off: s = 0, no key, chosen (lower index first) only where
  * the groups that stay have fewer than k others; a token without open experts gets weights 0.  A
  * bias at or below -1e30 makes its expert the last choice likewise, with its score.  A logit that is
